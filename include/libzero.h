@@ -720,6 +720,162 @@ zero_status zero_sched_wait(zero_sched* s, zero_stream_t stream);
 zero_status zero_sched_launches(const zero_sched* s, uint64_t* count);
 void zero_sched_destroy(zero_sched* s);
 
+/* ------------------------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits. "ZeRO: particionar estados do treino entre GPUs"
+ * (upskillscore.com), "Como funciona": what the partitioned model states leave is the memory of
+ * the activation checkpoints (ZeRO-R). The pages give no format; this library's keeps
+ * zero_quantize_q8's rule per block of 128 columns of a row:
+ *   scale = amax/127 (binary32), q = round_half_even(x/scale) clamped to [-127, 127], 0 where
+ *   scale is 0; a block with an inf or NaN gets scale NaN and q = 0 (a gradient made from it is
+ *   NaN, so the step is skipped as on any overflow).
+ * A checkpoint of rows x cols values is rows records of ZERO_CKPT_ROW_BYTES(cols) bytes:
+ *   cols bytes q + 128, filled up to a multiple of 16 with 128 (q = 0); ceil(cols/128) fp32
+ *   scales; zeros up to a multiple of 32.
+ * A record holds a whole row: any range of rows is a checkpoint of its own (row r0's address is
+ * base + r0*ZERO_CKPT_ROW_BYTES(cols)), so checkpoints can be split among ranks by rows.
+ * ---------------------------------------------------------------------------------------- */
+#define ZERO_CKPT_CODE_BYTES(cols) (((uint64_t)(cols) + 15u) / 16u * 16u)
+#define ZERO_CKPT_ROW_BYTES(cols) \
+    ((ZERO_CKPT_CODE_BYTES(cols) + ((uint64_t)(cols) + 127u) / 128u * 4u + 31u) / 32u * 32u)
+
+/* Element types of activations, and of the parameters and gradients beside them. */
+typedef enum {
+    ZERO_F16 = 0,           /* IEEE binary16 */
+    ZERO_BF16 = 1,          /* bfloat16 */
+    ZERO_F32 = 2            /* IEEE binary32 */
+} zero_dtype;
+
+/* Write the checkpoint of x: rows x cols values of type `dtype`, row r at x + r*ldx (elements,
+ * ldx >= cols). x aligned to its element (16-byte aligned rows take the wide loads), ckpt
+ * 16-byte aligned, rows*ZERO_CKPT_ROW_BYTES(cols) bytes, not overlapping x.
+ * Errors: ZERO_EINVAL (null, unknown dtype, cols >= 2^31, ldx < cols, sizes that do not fit in
+ * 63 bits, overlap), ZERO_EALIGN, ZERO_ECUDA. rows or cols == 0 launches nothing. */
+zero_status zero_ckpt_save_q8(uint64_t rows, uint64_t cols, zero_dtype dtype, const void* x,
+                              uint64_t ldx, uint8_t* ckpt, zero_stream_t stream);
+
+/* Read a checkpoint back: out[r][c] = dtype(q*scale), the product in binary32, then rounded to
+ * nearest even. Same layout rules and errors as zero_ckpt_save_q8. */
+zero_status zero_ckpt_load_q8(uint64_t rows, uint64_t cols, const uint8_t* ckpt, zero_dtype dtype,
+                              void* out, uint64_t ldo, zero_stream_t stream);
+
+/* Weight gradient of a linear layer y = a W^T (W: out_features x in_features) from the 8-bit
+ * checkpoint of its input a:
+ *   dw[o][i] = sum over t of dy[t][o] * a[t][i]      (+ dw[o][i] if accumulate != 0)
+ * a[t][i] = the value zero_ckpt_load_q8 gives in dy's type; products summed in binary32 on the
+ * tensor cores in an order fixed by the sizes (the same call gives the same bits), rounded once
+ * to dw's type. dw may point into a gradient bucket: it is what zero_step_fused and the bucket
+ * schedulers take as a rank's gradient.
+ *   dtype     : ZERO_F16 or ZERO_BF16, the type of dy and dw
+ *   dy        : tokens x out_features, row stride lddy; dw: row stride lddw (elements). Aligned
+ *               to their elements; 16-byte aligned rows of dy take the tensor-map loads.
+ *   ckpt      : the checkpoint of a (tokens rows of in_features columns), 16-byte aligned
+ *   workspace : zero_ckpt_wgrad_q8_workspace(...) bytes (may be 0, then NULL is accepted),
+ *               16-byte aligned device memory, overwritten; calls that may run at the same time
+ *               need workspaces of their own
+ *   d_status  : ZERO_FLAG_TIMEOUT is ORed in if a wait inside the kernel gave up
+ * tokens == 0 writes zeros (or leaves dw with accumulate); out_features or in_features == 0
+ * launches nothing. Errors: ZERO_EINVAL (null, dtype, a feature count >= 2^30, tokens >= 2^31, a
+ * stride below its row, dw overlapping an input or the workspace), ZERO_EALIGN, ZERO_ENOMEM
+ * (workspace too small), ZERO_ECUDA. */
+zero_status zero_ckpt_wgrad_q8_workspace(uint64_t tokens, uint64_t out_features,
+                                         uint64_t in_features, uint64_t* bytes);
+zero_status zero_ckpt_wgrad_q8(uint64_t tokens, uint64_t out_features, uint64_t in_features,
+                               zero_dtype dtype, const void* dy, uint64_t lddy,
+                               const uint8_t* ckpt, void* dw, uint64_t lddw, int accumulate,
+                               void* workspace, uint64_t workspace_bytes, uint32_t* d_status,
+                               zero_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Block boundary: the norm after a block, its gate and residual scale, the residual addition,
+ * and the norm before the next block, in one pass over the rows, with the 8-bit checkpoints that
+ * the backward pass needs written on the way. For every row of rows x cols values:
+ *   y = residual_scale*x + branch_scale * gate (.) post(h)
+ *   u = pre(y)
+ * h is the block's output, x the residual stream before it, u the next block's input. post and
+ * pre are norms over the row's columns (z the row, w and b optional vectors of cols values):
+ *   ZERO_NORM_NONE  : z
+ *   ZERO_NORM_RMS   : z / sqrt(mean(z^2) + eps) * w + b
+ *   ZERO_NORM_LAYER : (z - mean(z)) / sqrt(var(z) + eps) * w + b      (var: over cols)
+ * All arithmetic is binary32; y (which pre reads before it is rounded) and u are rounded once.
+ *   gate  : row r uses gate row r / gate_rows (gate_rows = rows: one vector for every row;
+ *           = the sequence length: one per sequence; 1: one per row), row stride ldg;
+ *           gate_rows == 0: no gate (gate must be NULL)
+ *   x, h  : a matrix, or with x_ckpt / h_ckpt a checkpoint (exactly one of the two for x, at
+ *           most one for h). Without h: y = residual_scale*x, and the call is a norm of x (of a
+ *           checkpoint: the recomputation of a block's input); post_norm must then be NONE and
+ *           gate, post_w, post_b NULL.
+ *   y, u, save_y, save_h : outputs, each may be NULL (not all of them). save_y and save_h are
+ *           the checkpoints of y as stored (rounded to dtype) and of h, byte for byte what
+ *           zero_ckpt_save_q8 writes for them; save_h needs h as a matrix; u needs a pre_norm.
+ * Matrices: dtype, element-aligned, row strides ld* in elements (>= cols); vectors (post_w ...)
+ * contiguous; checkpoints 16-byte aligned. y may be x itself (same address and stride); no other
+ * output may overlap an input or another output.
+ * Errors: ZERO_EINVAL (the rules above, cols > ZERO_JOIN_MAX_COLS, unknown dtype or norm, eps
+ * negative or not finite, scales not finite, overlap), ZERO_EALIGN, ZERO_ECUDA. rows or
+ * cols == 0 launches nothing.
+ * ---------------------------------------------------------------------------------------- */
+#define ZERO_JOIN_MAX_COLS 16384
+
+typedef enum {
+    ZERO_NORM_NONE = 0,
+    ZERO_NORM_RMS = 1,
+    ZERO_NORM_LAYER = 2
+} zero_norm;
+
+/* What a boundary's forward and backward calls share. */
+typedef struct {
+    uint64_t rows, cols;
+    zero_dtype dtype;            /* of every matrix and vector of the call */
+    zero_norm post_norm, pre_norm;
+    float post_eps, pre_eps;
+    float residual_scale, branch_scale;
+    uint64_t gate_rows;          /* rows that share one gate vector; 0: no gate */
+    const void* gate;            /* ceil(rows/gate_rows) rows of cols values */
+    uint64_t ldg;
+    const void *post_w, *post_b; /* cols values each, or NULL (1 and 0) */
+    const void *pre_w, *pre_b;
+} zero_block_desc;
+
+zero_status zero_block_join(const zero_block_desc* desc, const void* x, uint64_t ldx,
+                            const uint8_t* x_ckpt, const void* h, uint64_t ldh,
+                            const uint8_t* h_ckpt, void* y, uint64_t ldy, void* u, uint64_t ldu,
+                            uint8_t* save_y, uint8_t* save_h, zero_stream_t stream);
+
+/* Gradient of zero_block_join at the saved y and h (each a matrix or a checkpoint; the norms'
+ * statistics are computed from them again), given dy (the gradient arriving along the residual
+ * stream; NULL: zero) and du (the gradient of u; NULL: zero):
+ *   gy = dy + (gradient of pre at y applied to du);  dx = residual_scale*gy
+ *   t  = branch_scale * gate (.) gy;                 dh = gradient of post at h applied to t
+ *   dpre_w = sum over rows of du (.) (y normalised), dpre_b = sum of du; dpost_w, dpost_b the
+ *   same of t and h; dgate[k] = sum over gate row k's rows of branch_scale * gy (.) post(h)
+ * The sums run in binary32 in an order fixed by the sizes (no atomics: the same call gives the
+ * same bits) and are rounded once to dtype.
+ *   y / y_ckpt : needed if du is given; h / h_ckpt: needed with a post_norm or dgate
+ *   dx, dh, dgate (stride lddg), dpost_w, dpost_b, dpre_w, dpre_b: outputs, each may be NULL
+ *                (not all of them); dgate needs a gate, dpost_* a branch (dh's rules), dpre_* a
+ *                pre_norm. dx may be dy itself (same address and stride).
+ *   accumulate : ZERO_ACC_PARAMS: dpost_*, dpre_* are added to what they hold; ZERO_ACC_GATE:
+ *                dgate too (micro-batches; the sum is rounded once)
+ *   has_branch : 0 for a boundary without h (dh, dgate, dpost_* NULL), else 1
+ *   workspace  : zero_block_join_backward_workspace(...) bytes, 16-byte aligned device memory,
+ *                overwritten; calls that may run at the same time need workspaces of their own.
+ *                It may be NULL if no vector gradient is asked for.
+ * rows == 0 writes zeros into the vector gradients (accumulate leaves them; dgate has no rows).
+ * Errors: as zero_block_join, and ZERO_ENOMEM for a workspace that is too small. */
+#define ZERO_ACC_PARAMS 1
+#define ZERO_ACC_GATE 2
+
+zero_status zero_block_join_backward_workspace(uint64_t rows, uint64_t cols, uint64_t gate_rows,
+                                               uint64_t* bytes);
+zero_status zero_block_join_backward(const zero_block_desc* desc, int has_branch, const void* y,
+                                     uint64_t ldy, const uint8_t* y_ckpt, const void* h,
+                                     uint64_t ldh, const uint8_t* h_ckpt, const void* dy,
+                                     uint64_t lddy, const void* du, uint64_t lddu, void* dx,
+                                     uint64_t lddx, void* dh, uint64_t lddh, void* dgate,
+                                     uint64_t lddg, void* dpost_w, void* dpost_b, void* dpre_w,
+                                     void* dpre_b, int accumulate, void* workspace,
+                                     uint64_t workspace_bytes, zero_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,10 +34,20 @@ ZERO_MAX_RANKS = 64
 ZERO_Q8_BLOCK = 128
 ZERO_Q8_RECORD = 132
 
+ZERO_F16, ZERO_BF16, ZERO_F32 = 0, 1, 2
+ZERO_NORM_NONE, ZERO_NORM_RMS, ZERO_NORM_LAYER = 0, 1, 2
+ZERO_JOIN_MAX_COLS = 16384
+ZERO_ACC_PARAMS, ZERO_ACC_GATE = 1, 2
+
 
 def q8_payload_bytes(n: int) -> int:
     """ZERO_Q8_PAYLOAD_BYTES(n)."""
     return (n + 127) // 128 * 132
+
+
+def ckpt_row_bytes(cols: int) -> int:
+    """ZERO_CKPT_ROW_BYTES(cols)."""
+    return ((cols + 15) // 16 * 16 + (cols + 127) // 128 * 4 + 31) // 32 * 32
 
 # every symbol include/libzero.h declares
 SYMBOLS = (
@@ -61,6 +71,9 @@ SYMBOLS = (
     "zero_layer_sched_buf_elems", "zero_layer_sched_create", "zero_layer_sched_begin_step",
     "zero_layer_sched_acquire", "zero_layer_sched_release", "zero_layer_sched_gathers",
     "zero_layer_sched_destroy",
+    "zero_ckpt_save_q8", "zero_ckpt_load_q8", "zero_ckpt_wgrad_q8_workspace",
+    "zero_ckpt_wgrad_q8", "zero_block_join", "zero_block_join_backward_workspace",
+    "zero_block_join_backward",
 )
 
 
@@ -125,6 +138,16 @@ class FusedQ8Range(C.Structure):
 class ScalerParams(C.Structure):
     _fields_ = [("growth_factor", C.c_float), ("backoff_factor", C.c_float),
                 ("growth_interval", C.c_int32)]
+
+
+class BlockDesc(C.Structure):
+    """zero_block_desc: what a block boundary's forward and backward calls share."""
+    _fields_ = [("rows", C.c_uint64), ("cols", C.c_uint64), ("dtype", C.c_int),
+                ("post_norm", C.c_int), ("pre_norm", C.c_int), ("post_eps", C.c_float),
+                ("pre_eps", C.c_float), ("residual_scale", C.c_float),
+                ("branch_scale", C.c_float), ("gate_rows", C.c_uint64), ("gate", C.c_void_p),
+                ("ldg", C.c_uint64), ("post_w", C.c_void_p), ("post_b", C.c_void_p),
+                ("pre_w", C.c_void_p), ("pre_b", C.c_void_p)]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -214,6 +237,17 @@ def _load():
     L.zero_layer_sched_release.argtypes = [vp, i32, vp]
     L.zero_layer_sched_gathers.argtypes = [vp, P(u64)]
     L.zero_layer_sched_destroy.argtypes, L.zero_layer_sched_destroy.restype = [vp], None
+    L.zero_ckpt_save_q8.argtypes = [u64, u64, i32, vp, u64, vp, vp]
+    L.zero_ckpt_load_q8.argtypes = [u64, u64, vp, i32, vp, u64, vp]
+    L.zero_ckpt_wgrad_q8_workspace.argtypes = [u64, u64, u64, P(u64)]
+    L.zero_ckpt_wgrad_q8.argtypes = [u64, u64, u64, i32, vp, u64, vp, vp, u64, i32, vp, u64, vp,
+                                     vp]
+    L.zero_block_join.argtypes = [P(BlockDesc), vp, u64, vp, vp, u64, vp, vp, u64, vp, u64, vp,
+                                  vp, vp]
+    L.zero_block_join_backward_workspace.argtypes = [u64, u64, u64, P(u64)]
+    L.zero_block_join_backward.argtypes = [P(BlockDesc), i32, vp, u64, vp, vp, u64, vp, vp, u64,
+                                           vp, u64, vp, u64, vp, u64, vp, u64, vp, vp, vp, vp,
+                                           i32, vp, u64, vp]
     # every other entry point returns a zero_status: ctypes' default int restype
     return L
 
@@ -804,3 +838,167 @@ def zero_sched_destroy(s: Sched):
     if s.handle:
         _lib.zero_sched_destroy(s.handle)
         s.handle = None
+
+
+# ---------------------------------------------------------------------------------------------
+# activations: 8-bit checkpoints, the block boundary, the weight gradient from a checkpoint
+# ---------------------------------------------------------------------------------------------
+_DTYPE_CODES: dict = {}
+_NORM_CODES = {"none": ZERO_NORM_NONE, "rms": ZERO_NORM_RMS, "layer": ZERO_NORM_LAYER}
+
+
+def _dtype(x) -> int | None:
+    """The zero_dtype of a tensor, None of an address."""
+    if not hasattr(x, "data_ptr"):
+        return None
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16,
+                             torch.float32: ZERO_F32})
+    code = _DTYPE_CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"expected float16, bfloat16 or float32, got {x.dtype}")
+    return code
+
+
+def _dtype_of(xs, dtype) -> int:
+    """The one zero_dtype of the tensors among xs (`dtype` where all are addresses)."""
+    for x in xs:
+        code = _dtype(x)
+        if code is None:
+            continue
+        if dtype is None:
+            dtype = code
+        elif code != dtype:
+            raise TypeError("tensors of different types in one call")
+    if dtype is None:
+        raise TypeError("dtype is needed where every operand is an address")
+    return dtype
+
+
+def _mat(x, rows: int, cols: int):
+    """(address, row stride) of a rows x cols operand: a tensor whose columns are adjacent (its
+    rows may be strided), (address, stride), or an address of adjacent rows."""
+    if x is None:
+        return 0, cols
+    if hasattr(x, "data_ptr"):
+        if tuple(x.shape) != (rows, cols):
+            raise TypeError(f"expected a {rows} x {cols} tensor, got {tuple(x.shape)}")
+        s0, s1 = x.stride()
+        if s1 != 1 and cols > 1:
+            raise TypeError("the columns of a matrix must be adjacent")
+        return int(x.data_ptr()), int(s0) if rows > 1 else max(int(s0), cols)
+    if isinstance(x, tuple):
+        return int(x[0]), int(x[1])
+    return int(x), cols
+
+
+def _ckpt(x, rows: int, cols: int) -> int:
+    if x is not None and hasattr(x, "data_ptr") and \
+            x.numel() * x.element_size() < rows * ckpt_row_bytes(cols):
+        raise TypeError("checkpoint buffer smaller than rows * ckpt_row_bytes(cols)")
+    return _ptr(x, 1)
+
+
+def _vec(x, cols: int) -> int:
+    if x is not None and hasattr(x, "data_ptr") and x.numel() != cols:
+        raise TypeError(f"expected a vector of {cols} values, got {tuple(x.shape)}")
+    return _ptr(x)
+
+
+def _nbytes(x, given=None) -> int:
+    if given is not None:
+        return given
+    return 0 if x is None else x.numel() * x.element_size()
+
+
+def zero_ckpt_save_q8(rows: int, cols: int, x, ckpt, dtype: int | None = None, stream=None):
+    """x: a rows x cols tensor (rows may be strided), or (address, stride) with dtype."""
+    p, ld = _mat(x, rows, cols)
+    _check(_lib.zero_ckpt_save_q8(rows, cols, _dtype_of((x,), dtype), p, ld,
+                                  _ckpt(ckpt, rows, cols), _stream(stream)),
+           "zero_ckpt_save_q8")
+
+
+def zero_ckpt_load_q8(rows: int, cols: int, ckpt, out, dtype: int | None = None, stream=None):
+    p, ld = _mat(out, rows, cols)
+    _check(_lib.zero_ckpt_load_q8(rows, cols, _ckpt(ckpt, rows, cols), _dtype_of((out,), dtype),
+                                  p, ld, _stream(stream)), "zero_ckpt_load_q8")
+
+
+def zero_ckpt_wgrad_q8_workspace(tokens: int, out_features: int, in_features: int) -> int:
+    out = C.c_uint64()
+    _check(_lib.zero_ckpt_wgrad_q8_workspace(tokens, out_features, in_features, C.byref(out)),
+           "zero_ckpt_wgrad_q8_workspace")
+    return out.value
+
+
+def zero_ckpt_wgrad_q8(tokens: int, out_features: int, in_features: int, dy, ckpt, dw, d_status,
+                       workspace=None, workspace_bytes: int | None = None,
+                       accumulate: bool = False, dtype: int | None = None, stream=None):
+    """dy: tokens x out_features, dw: out_features x in_features (tensors whose rows may be
+    strided, or (address, stride) with dtype); workspace_bytes where workspace is an address."""
+    pdy, lddy = _mat(dy, tokens, out_features)
+    pdw, lddw = _mat(dw, out_features, in_features)
+    _check(_lib.zero_ckpt_wgrad_q8(tokens, out_features, in_features, _dtype_of((dy, dw), dtype),
+                                   pdy, lddy, _ckpt(ckpt, tokens, in_features), pdw, lddw,
+                                   1 if accumulate else 0, _ptr(workspace),
+                                   _nbytes(workspace, workspace_bytes), _ptr(d_status, 4),
+                                   _stream(stream)), "zero_ckpt_wgrad_q8")
+
+
+def _block_desc(rows, cols, dtype, post_norm, pre_norm, post_eps, pre_eps, residual_scale,
+                branch_scale, gate, gate_rows, post_w, post_b, pre_w, pre_b) -> BlockDesc:
+    g, ldg = _mat(gate, -(-rows // gate_rows) if gate_rows else 0, cols)
+    return BlockDesc(rows, cols, dtype, _NORM_CODES.get(post_norm, post_norm),
+                     _NORM_CODES.get(pre_norm, pre_norm), post_eps, pre_eps, residual_scale,
+                     branch_scale, gate_rows, g, ldg, _vec(post_w, cols), _vec(post_b, cols),
+                     _vec(pre_w, cols), _vec(pre_b, cols))
+
+
+def zero_block_join(rows: int, cols: int, *, x=None, x_ckpt=None, h=None, h_ckpt=None, y=None,
+                    u=None, save_y=None, save_h=None, post_norm="none", pre_norm="none",
+                    post_eps: float = 1e-5, pre_eps: float = 1e-5, residual_scale: float = 1.0,
+                    branch_scale: float = 1.0, gate=None, gate_rows: int = 0, post_w=None,
+                    post_b=None, pre_w=None, pre_b=None, dtype: int | None = None, stream=None):
+    """Matrices and the gate: tensors whose rows may be strided, or (address, stride) with
+    dtype. post_norm, pre_norm: "none", "rms", "layer" or ZERO_NORM_*."""
+    d = _block_desc(rows, cols, _dtype_of((x, h, y, u, gate, post_w, post_b, pre_w, pre_b), dtype),
+                    post_norm, pre_norm, post_eps, pre_eps, residual_scale, branch_scale, gate,
+                    gate_rows, post_w, post_b, pre_w, pre_b)
+    _check(_lib.zero_block_join(C.byref(d), *_mat(x, rows, cols), _ckpt(x_ckpt, rows, cols),
+                                *_mat(h, rows, cols), _ckpt(h_ckpt, rows, cols),
+                                *_mat(y, rows, cols), *_mat(u, rows, cols),
+                                _ckpt(save_y, rows, cols), _ckpt(save_h, rows, cols),
+                                _stream(stream)), "zero_block_join")
+
+
+def zero_block_join_backward_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
+    out = C.c_uint64()
+    _check(_lib.zero_block_join_backward_workspace(rows, cols, gate_rows, C.byref(out)),
+           "zero_block_join_backward_workspace")
+    return out.value
+
+
+def zero_block_join_backward(rows: int, cols: int, *, y=None, y_ckpt=None, h=None, h_ckpt=None,
+                             dy=None, du=None, dx=None, dh=None, dgate=None, dpost_w=None,
+                             dpost_b=None, dpre_w=None, dpre_b=None, has_branch: bool = True,
+                             accumulate: int = 0, workspace=None,
+                             workspace_bytes: int | None = None, post_norm="none",
+                             pre_norm="none", post_eps: float = 1e-5, pre_eps: float = 1e-5,
+                             residual_scale: float = 1.0, branch_scale: float = 1.0, gate=None,
+                             gate_rows: int = 0, post_w=None, post_b=None, pre_w=None, pre_b=None,
+                             dtype: int | None = None, stream=None):
+    d = _block_desc(rows, cols,
+                    _dtype_of((y, h, dy, du, dx, dh, dgate, dpost_w, dpost_b, dpre_w, dpre_b,
+                               gate, post_w, post_b, pre_w, pre_b), dtype),
+                    post_norm, pre_norm, post_eps, pre_eps, residual_scale, branch_scale, gate,
+                    gate_rows, post_w, post_b, pre_w, pre_b)
+    gates = -(-rows // gate_rows) if gate_rows else 0
+    _check(_lib.zero_block_join_backward(
+        C.byref(d), 1 if has_branch else 0, *_mat(y, rows, cols), _ckpt(y_ckpt, rows, cols),
+        *_mat(h, rows, cols), _ckpt(h_ckpt, rows, cols), *_mat(dy, rows, cols),
+        *_mat(du, rows, cols), *_mat(dx, rows, cols), *_mat(dh, rows, cols),
+        *_mat(dgate, gates, cols), _vec(dpost_w, cols), _vec(dpost_b, cols), _vec(dpre_w, cols),
+        _vec(dpre_b, cols), accumulate, _ptr(workspace), _nbytes(workspace, workspace_bytes),
+        _stream(stream)), "zero_block_join_backward")
