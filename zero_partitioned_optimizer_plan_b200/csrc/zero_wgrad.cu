@@ -117,29 +117,19 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
     return r;
 }
 
+// Arrive on a barrier of the pair. What the arrival publishes was written before a proxy fence
+// (operand tiles, which only the tensor cores read) or waited for (tensor memory reads), so the
+// arrival itself needs no fence of cluster scope: that one waits for the copies in flight too,
+// and made the kernel 2.5 times slower.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// mbar_wait with cluster scope (the other CTA arrives on these barriers too), in line: a call
-// would first wait for every load the caller has in flight.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+// mbar_wait in line.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if ((i & 63u) == 0) {
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
@@ -431,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                 const Unit u = unit_at(p.plan, n);
                 for (uint32_t kb = u.kb0; kb < u.kb1; ++kb, ++it) {
                     const uint32_t s = it % kStages, use = it / kStages;
-                    ok = wait_cluster(&hd.empty[s], (use & 1u) ^ 1u);
+                    ok = wait_on(&hd.empty[s], (use & 1u) ^ 1u);
                     if (!ok) break;
                     const uint32_t dst = tiles + s * kStageBytes;
                     const int y = (int)(kb * kTileK), col = (int)(u.i0 + rank * kHalf);
@@ -455,13 +445,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             for (uint64_t n = pair; ok && n < p.plan.units; n += pairs, ++tile) {
                 const Unit u = unit_at(p.plan, n);
                 const uint32_t b = tile & 1u;
-                ok = wait_cluster(&hd.acc_empty[b], ((tile >> 1) & 1u) ^ 1u);
+                ok = wait_on(&hd.acc_empty[b], ((tile >> 1) & 1u) ^ 1u);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + b * kTileI;
                 for (uint32_t kb = u.kb0; kb < u.kb1; ++kb, ++it) {
                     const uint32_t s = it % kStages;
-                    ok = wait_cluster(&hd.full[s], (it / kStages) & 1u);
+                    ok = wait_on(&hd.full[s], (it / kStages) & 1u);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t st = tiles + s * kStageBytes;
@@ -483,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             for (uint32_t kb = u.kb0; kb < u.kb1; ++kb, ++it) {
                 const uint32_t s = it % kStages, st = tiles + s * kStageBytes;
                 // the stage's codes were asked for after its last products ended
-                ok = __all_sync(0xffffffffu, wait_cluster(&hd.raw[s], (it / kStages) & 1u));
+                ok = __all_sync(0xffffffffu, wait_on(&hd.raw[s], (it / kStages) & 1u));
                 if (!ok) break;
                 convert_stage<T>(st, lane, w, scale);
                 if (!kTma)
@@ -497,13 +487,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         // the last use of every stage: no arrival may reach a CTA that has left
         for (uint32_t j = it < kStages ? 0 : it - kStages; ok && j < it; ++j)
             ok = __all_sync(0xffffffffu,
-                            wait_cluster(&hd.empty[j % kStages], (j / kStages) & 1u));
+                            wait_on(&hd.empty[j % kStages], (j / kStages) & 1u));
     } else {   // the four warps that write results: lanes 32*warp .. of tensor memory
         uint32_t tile = 0;
         for (uint64_t n = pair; ok && n < p.plan.units; n += pairs, ++tile) {
             const Unit u = unit_at(p.plan, n);
             const uint32_t b = tile & 1u;
-            ok = __all_sync(0xffffffffu, wait_cluster(&hd.acc_full[b], (tile >> 1) & 1u));
+            ok = __all_sync(0xffffffffu, wait_on(&hd.acc_full[b], (tile >> 1) & 1u));
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t row = rank * kHalf + 32u * warp + lane;
