@@ -27,33 +27,46 @@ namespace zk {
 
 namespace {
 
-constexpr uint32_t kTileO = 256, kTileI = 256;   // outputs per pair of CTAs
+constexpr uint32_t kTileI = 256;                 // in-features per pair of CTAs
 constexpr uint32_t kTileK = 64;                  // tokens per stage
-constexpr int kStages = 5;
 constexpr uint32_t kHalf = 128;                  // features per CTA of either operand
 constexpr uint32_t kOpBytes = kHalf * kTileK * 2;        // one operand's stage in one CTA
 constexpr uint32_t kCodeBytes = kHalf * kTileK;      // a stage's codes in one CTA
-constexpr uint32_t kScaleBytes = 16 * kTileK;        // 4 neighbouring scales per token
-constexpr uint32_t kRawAt = 2 * kOpBytes, kScaleAt = kRawAt + kCodeBytes;
-constexpr uint32_t kStageBytes = kScaleAt + kScaleBytes;
 constexpr uint32_t kGroupBytes = kTileK * 128;   // 64 features (128 bytes) x 64 tokens
 constexpr int kEpiWarps = 4, kConvWarps = 8;
-constexpr int kTmaWarp = 4, kMmaWarp = 5, kConvWarp0 = 6;
+constexpr int kTmaWarp = 4, kMmaWarp = 5, kScaleWarp = 6, kConvWarp0 = 7;
 constexpr int kWgradThreads = 32 * (kConvWarp0 + kConvWarps);
-constexpr uint32_t kHeadBytes = 1024;            // barriers, tensor-memory address
-constexpr size_t kWgradSmem = kHeadBytes + (size_t)kStages * kStageBytes + 1024;
-static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
+constexpr uint32_t kHeadBytes = 2048;            // barriers, tensor-memory address, scales
 
+// A pair's tile has kM * 256 out-features: kM = 1 keeps two accumulators in tensor memory (one
+// is written out while the next tile is computed), kM = 2 fills it with one and shares each
+// converted B tile between two products.
+template <int kM>
+struct Shape {
+    static constexpr uint32_t kTileO = 256 * kM;
+    static constexpr int kStages = kM == 2 ? 4 : 5;
+    static constexpr int kAccs = kM == 2 ? 1 : 2;
+    static constexpr uint32_t kBAt = kM * kOpBytes, kRawAt = kBAt + kOpBytes;
+    static constexpr uint32_t kStageBytes = kRawAt + kCodeBytes;
+    static constexpr size_t kSmem = kHeadBytes + (size_t)kStages * kStageBytes + 1024;
+    static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+constexpr int kMaxLoads = 5;
 struct Head {
-    uint64_t raw[kStages];       // each CTA: its codes and scales of a stage are there
-    uint64_t full[kStages];      // in the pair's first CTA: both CTAs' A and B of a stage are there
-    uint64_t empty[kStages];     // both: the products that read a stage are done
+    uint64_t raw[kMaxLoads];     // each CTA: its codes and scales of a stage are there
+    uint64_t full[kMaxLoads];    // in the pair's first CTA: both CTAs' A and B of a stage are there
+    uint64_t empty[kMaxLoads];   // both: the products that read a stage are done
     uint64_t acc_full[2];        // both: an accumulator is complete
     uint64_t acc_empty[2];       // first CTA: both CTAs have read an accumulator
     uint32_t tmem;
+    float scale[kMaxLoads][kTileK];   // of this CTA's 128 features, per token
 };
+static_assert(sizeof(Head) <= kHeadBytes, "head");
 
 struct WgradPlan {
+    uint32_t m;                  // 256 * m out-features per tile
     uint32_t tiles_o, tiles_i;   // output tiles
     uint32_t kblocks;            // stages of the whole sum
     uint32_t splits;             // parts of the sum
@@ -69,7 +82,8 @@ constexpr uint32_t kMinBlocks = 4;
 
 WgradPlan wgrad_plan(uint64_t t, uint64_t o, uint64_t i) {
     WgradPlan p;
-    p.tiles_o = (uint32_t)((o + kTileO - 1) / kTileO);
+    p.m = o > 256 ? 2 : 1;
+    p.tiles_o = (uint32_t)((o + 256 * p.m - 1) / (256 * p.m));
     p.tiles_i = (uint32_t)((i + kTileI - 1) / kTileI);
     p.kblocks = (uint32_t)((t + kTileK - 1) / kTileK);
     const uint64_t tiles = (uint64_t)p.tiles_o * p.tiles_i;
@@ -90,7 +104,7 @@ WgradPlan wgrad_plan(uint64_t t, uint64_t o, uint64_t i) {
 
 uint64_t wgrad_workspace(uint64_t t, uint64_t o, uint64_t i) {
     const WgradPlan p = wgrad_plan(t, o, i);
-    return p.splits > 1 ? (uint64_t)p.tiles_o * p.tiles_i * p.splits * kTileO * kTileI * 4 : 0;
+    return p.splits > 1 ? (uint64_t)p.tiles_o * p.tiles_i * p.splits * 256 * p.m * kTileI * 4 : 0;
 }
 
 namespace {
@@ -174,7 +188,7 @@ template <typename T>
 __device__ __forceinline__ constexpr uint32_t mma_desc() {
     constexpr uint32_t fmt = std::is_same<T, bf16>::value ? 1u : 0u;
     return 1u << 4 | fmt << 7 | fmt << 10 | 1u << 15 | 1u << 16 | (kTileI >> 3) << 17 |
-           (kTileO >> 4) << 24;
+           (256u >> 4) << 24;
 }
 
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -222,7 +236,7 @@ struct WgradCall {
 };
 
 struct WgradMaps {
-    CUtensorMap dy, codes, scales;
+    CUtensorMap dy, codes;
 };
 
 struct Unit {
@@ -238,7 +252,7 @@ __device__ __forceinline__ Unit unit_at(const WgradPlan& p, uint64_t n) {
     const uint32_t in_band = tile - band * 8 * p.tiles_o;
     const uint32_t width = min(8u, p.tiles_i - band * 8);
     Unit u;
-    u.o0 = in_band / width * kTileO;
+    u.o0 = in_band / width * 256u * p.m;
     u.i0 = (band * 8 + in_band % width) * kTileI;
     u.kb0 = part * p.split_blocks;
     u.kb1 = min(u.kb0 + p.split_blocks, p.kblocks);
@@ -288,17 +302,24 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ float ld_shared_f(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+// 4 bytes global -> shared memory without a register (zeros where !there).
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 4 : 0)
+                 : "memory");
+}
+
+// Arrive on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
 
 // A stage's codes to T: lane l of warp w takes columns 16*(l%8) .. of token rows 4w + l/8 and
-// 32 + 4w + l/8. `scale`: the block's place among the four scales of a row.
+// 32 + 4w + l/8.
 template <typename T>
-__device__ __forceinline__ void convert_stage(uint32_t st, uint32_t lane, uint32_t w,
-                                              uint32_t scale) {
+__device__ __forceinline__ void convert_stage(uint32_t raw, const float* scale, uint32_t tile,
+                                              uint32_t lane, uint32_t w) {
     const uint32_t k0 = 4u * w + (lane >> 3), ch = 2u * (lane & 7u);
     // lanes of the second group of 64 features store their chunks in the other order: a quarter
     // warp then covers all eight 16-byte columns of the banks
@@ -307,8 +328,8 @@ __device__ __forceinline__ void convert_stage(uint32_t st, uint32_t lane, uint32
     float s[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        q[j] = ld_shared16(st + kRawAt + (k0 + 32u * j) * kHalf + 8u * ch);
-        s[j] = ld_shared_f(st + kScaleAt + (k0 + 32u * j) * 16u + 4u * scale);
+        q[j] = ld_shared16(raw + (k0 + 32u * j) * kHalf + 8u * ch);
+        s[j] = *(volatile const float*)(scale + k0 + 32u * j);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -316,8 +337,8 @@ __device__ __forceinline__ void convert_stage(uint32_t st, uint32_t lane, uint32
         const uint2 a = widen4<T>(q[j].x, s[j]), b = widen4<T>(q[j].y, s[j]);
         const uint2 d = widen4<T>(q[j].z, s[j]), e = widen4<T>(q[j].w, s[j]);
         const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
-        st_shared16(st + kOpBytes + chunk_at(ch + swap, k), swap ? hi : lo);
-        st_shared16(st + kOpBytes + chunk_at(ch + 1u - swap, k), swap ? lo : hi);
+        st_shared16(tile + chunk_at(ch + swap, k), swap ? hi : lo);
+        st_shared16(tile + chunk_at(ch + 1u - swap, k), swap ? lo : hi);
     }
 }
 
@@ -376,9 +397,12 @@ __device__ __forceinline__ void store_row(T* p, const uint32_t (&v)[32], uint32_
         }
 }
 
-template <typename T, bool kTma>
+template <typename T, bool kTma, int kM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     wgrad_kernel(const __grid_constant__ WgradCall p, const __grid_constant__ WgradMaps maps) {
+    using S = Shape<kM>;
+    constexpr int kStages = S::kStages, kAccs = S::kAccs;
+    constexpr uint32_t kStageBytes = S::kStageBytes;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);   // swizzle atoms: 1024
     Head& hd = *reinterpret_cast<Head*>(base);
@@ -390,11 +414,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&hd.raw[s], 1);
+            mbar_init(&hd.raw[s], 1 + 32);
             mbar_init(&hd.full[s], (kTma ? 1 : 0) + 2 * kConvWarps);
             mbar_init(&hd.empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kAccs; ++b) {
             mbar_init(&hd.acc_full[b], 1);
             mbar_init(&hd.acc_empty[b], 2 * kEpiWarps);
         }
@@ -425,18 +449,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                     if (!ok) break;
                     const uint32_t dst = tiles + s * kStageBytes;
                     const int y = (int)(kb * kTileK), col = (int)(u.i0 + rank * kHalf);
-                    mbar_arrive_expect_tx(&hd.raw[s], kCodeBytes + kScaleBytes);
-                    tma_own(dst + kRawAt, &maps.codes, col, y, &hd.raw[s]);
-                    tma_own(dst + kScaleAt, &maps.scales,
-                            (int)p.a.ck.code_bytes + col / 512 * 16, y, &hd.raw[s]);
+                    mbar_arrive_expect_tx(&hd.raw[s], kCodeBytes);
+                    tma_own(dst + S::kRawAt, &maps.codes, col, y, &hd.raw[s]);
                     if (kTma) {
                         const uint32_t full = map_to(smem_addr(&hd.full[s]), 0);
-                        if (rank == 0) mbar_arrive_expect_tx(&hd.full[s], 2 * kOpBytes);
-                        const int x = (int)(u.o0 + rank * kHalf);
-                        tma_tile(dst, &maps.dy, x, y, full);
-                        tma_tile(dst + kGroupBytes, &maps.dy, x + 64, y, full);
+                        if (rank == 0) mbar_arrive_expect_tx(&hd.full[s], 2 * kM * kOpBytes);
+#pragma unroll
+                        for (int m = 0; m < kM; ++m) {
+                            const int x = (int)(u.o0 + m * 256 + rank * kHalf);
+                            const uint32_t at = dst + m * kOpBytes;
+                            tma_tile(at, &maps.dy, x, y, full);
+                            tma_tile(at + kGroupBytes, &maps.dy, x + 64, y, full);
+                        }
                     }
                 }
+            }
+        }
+    } else if (warp == kScaleWarp) {
+        uint32_t it = 0;
+        for (uint64_t n = pair; ok && n < p.plan.units; n += pairs) {
+            const Unit u = unit_at(p.plan, n);
+            const uint32_t block = (u.i0 + rank * kHalf) / 128u;
+            const uint32_t at = p.a.ck.code_bytes + 4u * min(block, p.a.ck.blocks - 1);
+            for (uint32_t kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+                const uint32_t s = it % kStages;
+                ok = __all_sync(0xffffffffu, wait_on(&hd.empty[s], ((it / kStages) & 1u) ^ 1u));
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t k = lane + 32u * j;
+                    const uint64_t t = (uint64_t)kb * kTileK + k;
+                    const bool there = t < p.a.tokens;
+                    copy4(smem_addr(&hd.scale[s][k]),
+                          p.a.ckpt + (there ? t : 0) * p.a.ck.row_bytes + at, there);
+                }
+                arrive_after_copies(&hd.raw[s]);
             }
         }
     } else if (warp == kMmaWarp) {
@@ -444,8 +491,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             uint32_t it = 0, tile = 0;
             for (uint64_t n = pair; ok && n < p.plan.units; n += pairs, ++tile) {
                 const Unit u = unit_at(p.plan, n);
-                const uint32_t b = tile & 1u;
-                ok = wait_on(&hd.acc_empty[b], ((tile >> 1) & 1u) ^ 1u);
+                const uint32_t b = tile % kAccs;
+                ok = wait_on(&hd.acc_empty[b], ((tile / kAccs) & 1u) ^ 1u);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + b * kTileI;
@@ -457,8 +504,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                     const uint32_t st = tiles + s * kStageBytes;
 #pragma unroll
                     for (uint32_t k = 0; k < kTileK / 16; ++k)   // 16 tokens = 2048 bytes
-                        mma_pair(d, tile_desc(st + k * 2048u), tile_desc(st + kOpBytes + k * 2048u),
-                                 mma_desc<T>(), kb > u.kb0 || k > 0);
+#pragma unroll
+                        for (uint32_t m = 0; m < kM; ++m)
+                            mma_pair(d + m * kTileI, tile_desc(st + m * kOpBytes + k * 2048u),
+                                     tile_desc(st + S::kBAt + k * 2048u), mma_desc<T>(),
+                                     kb > u.kb0 || k > 0);
                     commit_pair(&hd.empty[s]);
                 }
                 if (ok) commit_pair(&hd.acc_full[b]);
@@ -469,16 +519,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         uint32_t it = 0;
         for (uint64_t n = pair; ok && n < p.plan.units; n += pairs) {
             const Unit u = unit_at(p.plan, n);
-            const uint32_t scale = (u.i0 + rank * kHalf) / 128u & 3u;
             for (uint32_t kb = u.kb0; kb < u.kb1; ++kb, ++it) {
                 const uint32_t s = it % kStages, st = tiles + s * kStageBytes;
                 // the stage's codes were asked for after its last products ended
                 ok = __all_sync(0xffffffffu, wait_on(&hd.raw[s], (it / kStages) & 1u));
                 if (!ok) break;
-                convert_stage<T>(st, lane, w, scale);
+                convert_stage<T>(st + S::kRawAt, hd.scale[s], st + S::kBAt, lane, w);
                 if (!kTma)
-                    store_dy<T>(p.a, st, u.o0 + rank * kHalf, (uint64_t)kb * kTileK,
-                                w * 32u + lane);
+                    for (uint32_t m = 0; m < kM; ++m)
+                        store_dy<T>(p.a, st + m * kOpBytes, u.o0 + m * 256u + rank * kHalf,
+                                    (uint64_t)kb * kTileK, w * 32u + lane);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_at(map_to(smem_addr(&hd.full[s]), 0));
@@ -486,33 +536,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         }
         // the last use of every stage: no arrival may reach a CTA that has left
         for (uint32_t j = it < kStages ? 0 : it - kStages; ok && j < it; ++j)
-            ok = __all_sync(0xffffffffu,
-                            wait_on(&hd.empty[j % kStages], (j / kStages) & 1u));
+            ok = __all_sync(0xffffffffu, wait_on(&hd.empty[j % kStages], (j / kStages) & 1u));
     } else {   // the four warps that write results: lanes 32*warp .. of tensor memory
         uint32_t tile = 0;
         for (uint64_t n = pair; ok && n < p.plan.units; n += pairs, ++tile) {
             const Unit u = unit_at(p.plan, n);
-            const uint32_t b = tile & 1u;
-            ok = __all_sync(0xffffffffu, wait_on(&hd.acc_full[b], (tile >> 1) & 1u));
+            const uint32_t b = tile % kAccs;
+            ok = __all_sync(0xffffffffu, wait_on(&hd.acc_full[b], (tile / kAccs) & 1u));
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t row = rank * kHalf + 32u * warp + lane;
-            const uint32_t o = u.o0 + row;
 #pragma unroll 1
-            for (uint32_t c = 0; c < kTileI; c += 32) {
+            for (uint32_t c = 0; c < kM * kTileI; c += 32) {
+                const uint32_t row = c / kTileI * 256u + rank * kHalf + 32u * warp + lane;
+                const uint32_t o = u.o0 + row, i = u.i0 + c % kTileI;
                 uint32_t v[32];
                 tmem_load(tmem + b * kTileI + c + ((32u * warp) << 16), v);
                 if (p.partial) {
                     float4* out = reinterpret_cast<float4*>(
-                        p.partial + (n * kTileO + row) * kTileI + c);
+                        p.partial + (n * S::kTileO + row) * kTileI + c % kTileI);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         out[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
                                              __uint_as_float(v[4 * j + 2]),
                                              __uint_as_float(v[4 * j + 3]));
-                } else if (o < p.a.outf && u.i0 + c < p.a.inf) {
-                    store_row<T>((T*)p.a.dw.p + o * p.a.dw.ld + u.i0 + c, v, p.a.inf - u.i0 - c,
-                                 p.vec, p.a.accumulate != 0);
+                } else if (o < p.a.outf && i < p.a.inf) {
+                    store_row<T>((T*)p.a.dw.p + o * p.a.dw.ld + i, v, p.a.inf - i, p.vec,
+                                 p.a.accumulate != 0);
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -550,12 +599,12 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(WgradArgs a, WgradPlan 
         const uint32_t o = (uint32_t)(e / cols), i = (uint32_t)(e - (uint64_t)o * cols) * 4;
         float f[4] = {};
         if (partial) {
-            const uint32_t to = o / kTileO, ti = i / kTileI;
+            const uint32_t tile_o = 256 * plan.m, to = o / tile_o, ti = i / kTileI;
             const uint32_t band = ti / 8, width = min(8u, plan.tiles_i - band * 8);
             const uint64_t tile = (uint64_t)band * 8 * plan.tiles_o + (uint64_t)to * width + ti % 8;
-            const float* src = partial + (tile * plan.splits * kTileO + o % kTileO) * kTileI + i % kTileI;
+            const float* src = partial + (tile * plan.splits * tile_o + o % tile_o) * kTileI + i % kTileI;
             for (uint32_t s = 0; s < plan.splits; ++s) {
-                const float4 v = *reinterpret_cast<const float4*>(src + (uint64_t)s * kTileO * kTileI);
+                const float4 v = *reinterpret_cast<const float4*>(src + (uint64_t)s * tile_o * kTileI);
                 f[0] = __fadd_rn(f[0], v.x);
                 f[1] = __fadd_rn(f[1], v.y);
                 f[2] = __fadd_rn(f[2], v.z);
@@ -603,7 +652,7 @@ cudaError_t encode_2d(EncodeFn encode, CUtensorMap* map, CUtensorMapDataType typ
 }
 
 // dy in boxes of 64 features x 64 tokens, swizzled; the checkpoint's bytes in boxes of 128 codes
-// and of 16 bytes of scales x 64 tokens. Zeros outside.
+// x 64 tokens. Zeros outside.
 cudaError_t make_maps(const WgradArgs& a, int dtype, bool tma, WgradMaps* m) {
     EncodeFn encode;
     cudaError_t e = encode_fn(&encode);
@@ -617,28 +666,26 @@ cudaError_t make_maps(const WgradArgs& a, int dtype, bool tma, WgradMaps* m) {
     if (e == cudaSuccess)
         e = encode_2d(encode, &m->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck, rb, a.tokens, rb,
                       kHalf, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e == cudaSuccess)
-        e = encode_2d(encode, &m->scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, ck, rb, a.tokens, rb, 16,
-                      CU_TENSOR_MAP_SWIZZLE_NONE);
     return e;
 }
 
-template <typename T, bool kTma>
+template <typename T, bool kTma, int kM>
 cudaError_t run_pairs(const WgradCall& c, const WgradMaps& maps, int sms, cudaStream_t stream) {
-    auto kernel = wgrad_kernel<T, kTma>;
+    auto kernel = wgrad_kernel<T, kTma, kM>;
+    constexpr size_t smem = Shape<kM>::kSmem;
     thread_local int ready_on = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (ready_on != dev) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kWgradSmem);
+                                 (int)smem);
         if (e != cudaSuccess) return e;
         ready_on = dev;
     }
     const uint64_t most = (uint64_t)(sms / 2);
     const uint64_t pairs = c.plan.units < most ? c.plan.units : most;
-    return launch_act(kernel, dim3((unsigned)(2 * pairs)), kWgradThreads, kWgradSmem, stream, c,
+    return launch_act(kernel, dim3((unsigned)(2 * pairs)), kWgradThreads, smem, stream, c,
                       maps);
 }
 
@@ -657,8 +704,10 @@ cudaError_t run_wgrad(const WgradArgs& a, int dtype, void* ws, cudaStream_t stre
         WgradMaps maps = {};
         e = make_maps(a, dtype, tma, &maps);
         if (e != cudaSuccess) return e;
-        e = tma ? run_pairs<T, true>(c, maps, di.sms, stream)
-                : run_pairs<T, false>(c, maps, di.sms, stream);
+        e = c.plan.m == 2 ? (tma ? run_pairs<T, true, 2>(c, maps, di.sms, stream)
+                                 : run_pairs<T, false, 2>(c, maps, di.sms, stream))
+                          : (tma ? run_pairs<T, true, 1>(c, maps, di.sms, stream)
+                                 : run_pairs<T, false, 1>(c, maps, di.sms, stream));
         if (e != cudaSuccess || !c.partial) return e;
     }
     const uint64_t quads = (uint64_t)a.outf * ((a.inf + 3) / 4);
