@@ -33,8 +33,8 @@ constexpr uint32_t kHalf = 128;                  // features per CTA of either o
 constexpr uint32_t kOpBytes = kHalf * kTileK * 2;        // one operand's stage in one CTA
 constexpr uint32_t kCodeBytes = kHalf * kTileK;      // a stage's codes in one CTA
 constexpr uint32_t kGroupBytes = kTileK * 128;   // 64 features (128 bytes) x 64 tokens
-constexpr int kEpiWarps = 4, kConvWarps = 8;
-constexpr int kTmaWarp = 4, kMmaWarp = 5, kScaleWarp = 6, kConvWarp0 = 7;
+constexpr int kEpiWarps = 8, kConvWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kConvWarp0 = 11;
 constexpr int kWgradThreads = 32 * (kConvWarp0 + kConvWarps);
 constexpr uint32_t kHeadBytes = 2048;            // barriers, tensor-memory address, scales
 
@@ -74,30 +74,37 @@ struct WgradPlan {
     uint64_t units;              // tiles * splits
 };
 
-// Parts of the sum. A pair of CTAs works on one (tile, part) at a time and about kPairs of them
-// run at once; a part should leave at least kMinBlocks stages (a part's partial tile costs a
-// 256 KB write and read, about as much time as 16 stages).
-constexpr uint32_t kPairs = 74;
-constexpr uint32_t kMinBlocks = 4;
+constexpr uint32_t kPairs = 74;   // pairs of CTAs that run at once
 
+// Tile height and parts of the sum: the smallest modelled time over both heights and every split
+// that leaves the pairs at most two rounds. Measured on B200 (us): a stage 0.47 at 256 x 256 and
+// 0.62 at 512 x 256 (the taller tile is faster per output when it is filled); the start of a
+// tile's pipeline and its write-out 2.5 and 4; adding the parts, 3 for the second kernel and
+// 0.06 per 256 x 256 partial tile for its write and read.
 WgradPlan wgrad_plan(uint64_t t, uint64_t o, uint64_t i) {
-    WgradPlan p;
-    p.m = o > 256 ? 2 : 1;
-    p.tiles_o = (uint32_t)((o + 256 * p.m - 1) / (256 * p.m));
-    p.tiles_i = (uint32_t)((i + kTileI - 1) / kTileI);
-    p.kblocks = (uint32_t)((t + kTileK - 1) / kTileK);
-    const uint64_t tiles = (uint64_t)p.tiles_o * p.tiles_i;
-    uint64_t s = 1;
-    if (tiles && tiles < kPairs) {
-        s = kPairs / tiles;
-        const uint64_t most = p.kblocks / kMinBlocks;
-        if (s > most) s = most;
-        if (s < 1) s = 1;
+    WgradPlan best = {};
+    best.tiles_i = (uint32_t)((i + kTileI - 1) / kTileI);
+    best.kblocks = (uint32_t)((t + kTileK - 1) / kTileK);
+    float least = 0.0f;
+    for (uint32_t m = 1; m <= 2; ++m) {
+        const uint64_t tiles_o = (o + 256 * m - 1) / (256 * m), tiles = tiles_o * best.tiles_i;
+        for (uint64_t s = 1; s == 1 || (s <= best.kblocks && tiles * s <= 2 * kPairs); ++s) {
+            const uint64_t blocks = (best.kblocks + s - 1) / s;
+            const uint64_t parts = blocks ? (best.kblocks + blocks - 1) / blocks : 1;
+            const uint64_t units = tiles * parts, rounds = (units + kPairs - 1) / kPairs;
+            const float cost = (float)rounds * ((float)blocks * (m == 2 ? 0.62f : 0.47f) +
+                                                (m == 2 ? 4.0f : 2.5f)) +
+                               (parts > 1 ? 3.0f + 0.06f * (float)(units * m) : 0.0f);
+            if (best.m && cost >= least) continue;
+            least = cost;
+            best.m = m;
+            best.tiles_o = (uint32_t)tiles_o;
+            best.split_blocks = (uint32_t)blocks;
+            best.splits = (uint32_t)parts;
+            best.units = units;
+        }
     }
-    p.split_blocks = (uint32_t)((p.kblocks + s - 1) / s);
-    p.splits = p.split_blocks ? (p.kblocks + p.split_blocks - 1) / p.split_blocks : 1;
-    p.units = tiles * p.splits;
-    return p;
+    return best;
 }
 
 }  // namespace
@@ -150,6 +157,10 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity) {
             if (t - t0 > kWaitLimitNs) return false;
         }
     }
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // 2-D tile global -> this CTA's shared memory; the bytes count on a barrier of the pair.
@@ -412,6 +423,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     const uint32_t rank = cluster_rank();
     const uint64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
+    if (threadIdx.x == 32 * kTmaWarp) {
+        if (kTma) prefetch_map(&maps.dy);
+        prefetch_map(&maps.codes);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&hd.raw[s], 1 + 32);
@@ -537,7 +552,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         // the last use of every stage: no arrival may reach a CTA that has left
         for (uint32_t j = it < kStages ? 0 : it - kStages; ok && j < it; ++j)
             ok = __all_sync(0xffffffffu, wait_on(&hd.empty[j % kStages], (j / kStages) & 1u));
-    } else {   // the four warps that write results: lanes 32*warp .. of tensor memory
+    } else {   // write the results: lanes 32*(warp%4) .. of tensor memory, half of the columns
+        const uint32_t quarter = warp & 3u, first = (warp >> 2) * kM * kTileI / 2;
         uint32_t tile = 0;
         for (uint64_t n = pair; ok && n < p.plan.units; n += pairs, ++tile) {
             const Unit u = unit_at(p.plan, n);
@@ -546,11 +562,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-            for (uint32_t c = 0; c < kM * kTileI; c += 32) {
-                const uint32_t row = c / kTileI * 256u + rank * kHalf + 32u * warp + lane;
+            for (uint32_t c = first; c < first + kM * kTileI / 2; c += 32) {
+                const uint32_t row = c / kTileI * 256u + rank * kHalf + 32u * quarter + lane;
                 const uint32_t o = u.o0 + row, i = u.i0 + c % kTileI;
                 uint32_t v[32];
-                tmem_load(tmem + b * kTileI + c + ((32u * warp) << 16), v);
+                tmem_load(tmem + b * kTileI + c + (quarter << 21), v);
                 if (p.partial) {
                     float4* out = reinterpret_cast<float4*>(
                         p.partial + (n * S::kTileO + row) * kTileI + c % kTileI);
@@ -590,7 +606,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
 // dw = the parts of each tile added in order (+ dw), or zeros where there is no token.
 template <typename T>
 __global__ void __launch_bounds__(256) wgrad_join_kernel(WgradArgs a, WgradPlan plan,
-                                                         const float* partial) {
+                                                         const float* partial, int vec) {
     grid_wait();
     const uint32_t cols = (a.inf + 3) / 4;
     const uint64_t total = (uint64_t)a.outf * cols;
@@ -612,6 +628,17 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(WgradArgs a, WgradPlan 
             }
         }
         T* d = (T*)a.dw.p + o * a.dw.ld + i;
+        if (vec >= 8 && i + 4 <= a.inf) {
+            if (a.accumulate) {
+                const uint2 old = *reinterpret_cast<const uint2*>(d);
+                T t[4];
+                memcpy(t, &old, 8);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = __fadd_rn(to_f(t[j]), f[j]);
+            }
+            *reinterpret_cast<uint2*>(d) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+            continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (i + j < a.inf)
@@ -712,7 +739,7 @@ cudaError_t run_wgrad(const WgradArgs& a, int dtype, void* ws, cudaStream_t stre
     }
     const uint64_t quads = (uint64_t)a.outf * ((a.inf + 3) / 4);
     return launch_act(wgrad_join_kernel<T>, dim3(plain_grid(quads, di.sms)), 256, 0, stream, a,
-                      c.plan, (const float*)c.partial);
+                      c.plan, (const float*)c.partial, c.vec);
 }
 
 }  // namespace
