@@ -46,12 +46,54 @@ __device__ __forceinline__ float q8_scale(uint32_t amax) {
                                : __fdiv_rn(__uint_as_float(amax), 127.0f);
 }
 
-// Code byte of x. A scale of 0 or NaN gives q = 0. The quotient of a subnormal scale can pass
-// 127 (the scale itself was rounded): clamped.
+// Code byte of x by division. A scale of 0 or NaN gives q = 0. The quotient of a subnormal scale
+// can pass 127 (the scale itself was rounded): clamped.
 __device__ __forceinline__ uint32_t q8_code(float x, float scale) {
     if (!(scale > 0.0f)) return 128u;
     const int q = __float2int_rn(__fdiv_rn(x, scale));
     return (uint32_t)(min(max(q, -127), 127) + 128);
+}
+
+// The code bytes of the values x[0..7], as two words, from inv = fl(1/scale). For a scale of at
+// least 2^-100 the quotients stay below 127.5, and 1/scale lies strictly between inv*(1 - 2^-21)
+// and inv*(1 + 2^-21), wide enough that fl(x/scale) lies between the two products too: where
+// both products round to the same integer, fl(x/scale) rounds to it. (Rounding: the fused
+// multiply-add into 1.5 * 2^23 + 128 leaves the integer + 128 in the low byte.) The others, and
+// smaller, zero or NaN scales, take the division.
+constexpr float kQ8Bias = 12583040.0f;
+
+__device__ __noinline__ uint2 q8_codes_by_division(const float4 a, const float4 b, float scale) {
+    return make_uint2(q8_code(a.x, scale) | q8_code(a.y, scale) << 8 | q8_code(a.z, scale) << 16 |
+                          q8_code(a.w, scale) << 24,
+                      q8_code(b.x, scale) | q8_code(b.y, scale) << 8 | q8_code(b.z, scale) << 16 |
+                          q8_code(b.w, scale) << 24);
+}
+
+__device__ __forceinline__ uint2 q8_codes(const float (&x)[8], float scale, float inv) {
+    float c[8];
+    uint32_t differ = 0;
+    const float lo = __fmul_rn(inv, 1.0f - 0x1p-21f), hi = __fmul_rn(inv, 1.0f + 0x1p-21f);
+    const uint64_t l2 = f2_pack(lo, lo), h2 = f2_pack(hi, hi), bias = f2_pack(kQ8Bias, kQ8Bias);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const uint64_t v = f2_pack(x[j], x[j + 1]);
+        float a, b;
+        f2_unpack(f2_fma(v, l2, bias), a, b);
+        f2_unpack(f2_fma(v, h2, bias), c[j], c[j + 1]);
+        differ |= __float_as_uint(a) ^ __float_as_uint(c[j]);
+        differ |= __float_as_uint(b) ^ __float_as_uint(c[j + 1]);
+    }
+    if (!(scale >= 0x1p-100f) || differ != 0)
+        return q8_codes_by_division(make_float4(x[0], x[1], x[2], x[3]),
+                                    make_float4(x[4], x[5], x[6], x[7]), scale);
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t lo = __byte_perm(__float_as_uint(c[4 * k]), __float_as_uint(c[4 * k + 1]), 0x0040u);
+        const uint32_t hi = __byte_perm(__float_as_uint(c[4 * k + 2]), __float_as_uint(c[4 * k + 3]), 0x0040u);
+        w[k] = __byte_perm(lo, hi, 0x5410u);
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 __device__ __forceinline__ float q8_value(uint32_t byte, float scale) {
@@ -62,11 +104,319 @@ __device__ __forceinline__ const float* ckpt_scales(const uint8_t* row, const Ck
     return reinterpret_cast<const float*>(row + s.code_bytes);
 }
 
+// ---------------------------------------------------------------------------------------------
+// Eight columns per lane. A warp covers 256 columns (two blocks of codes) of a row. With 16-byte
+// aligned rows (kVec) a lane's columns are neighbours and move as 16-byte accesses; otherwise
+// lane l takes columns l, l + 32, ..., so that a warp's narrow accesses still touch whole sectors.
+// ---------------------------------------------------------------------------------------------
+constexpr uint32_t kWarpCols = 256;
+
+template <bool kVec>
+struct Cols {
+    uint32_t c0, cols;
+    uint32_t mask;   // bit j: column j exists
+    __device__ __forceinline__ Cols(uint32_t chunk, uint32_t lane, uint32_t n) : cols(n), mask(0) {
+        c0 = chunk * kWarpCols + (kVec ? 8u * lane : lane);
+        const uint32_t left = n > c0 ? n - c0 : 0u;
+        const uint32_t count = kVec ? left : (left + 31u) / 32u;
+        mask = count >= 8u ? 0xffu : (1u << count) - 1u;
+    }
+    __device__ __forceinline__ uint32_t at(int j) const { return c0 + (kVec ? j : 32 * j); }
+};
+
+// Eight values as they lie in memory: T, or codes (two words) and the scales of the lane's first
+// and second four columns.
+template <typename T>
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
+};
+
+template <typename T, bool kVec>
+__device__ __forceinline__ Raw<T> load_raw(const T* row, const Cols<kVec>& c) {
+    Raw<T> r;
+    if (kVec && c.mask == 0xffu) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + c.c0);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+            const uint4 q = p[k];
+            r.w[4 * k] = q.x;
+            r.w[4 * k + 1] = q.y;
+            r.w[4 * k + 2] = q.z;
+            r.w[4 * k + 3] = q.w;
+        }
+        return r;
+    }
+#pragma unroll
+    for (int k = 0; k < 2 * (int)sizeof(T); ++k) r.w[k] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (!(c.mask >> j & 1u)) continue;
+        if constexpr (sizeof(T) == 4) {
+            r.w[j] = reinterpret_cast<const uint32_t*>(row)[c.at(j)];
+        } else {
+            r.w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c.at(j)] << 16 * (j & 1);
+        }
+    }
+    return r;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ Raw<T> load_codes(const uint8_t* row, const CkptShape& s,
+                                             const Cols<kVec>& c) {
+    Raw<T> r;
+    r.w[0] = r.w[1] = 0x80808080u;
+    r.w[2] = r.w[3] = 0u;
+    if (c.mask == 0) return r;
+    const float* sc = ckpt_scales(row, s);
+    if constexpr (kVec) {
+        const uint2 q = *reinterpret_cast<const uint2*>(row + c.c0);
+        r.w[0] = q.x;
+        r.w[1] = q.y;
+        r.w[2] = r.w[3] = __float_as_uint(sc[c.c0 >> 7]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c.mask >> j & 1u) {
+                const uint32_t sh = 8 * (j & 3);
+                r.w[j / 4] = (r.w[j / 4] & ~(255u << sh)) | (uint32_t)row[c.at(j)] << sh;
+            }
+        r.w[2] = __float_as_uint(sc[c.c0 >> 7]);
+        if (c.mask & 0xf0u) r.w[3] = __float_as_uint(sc[(c.c0 >> 7) + 1]);
+    }
+    return r;
+}
+
+// Pairs of binary32 values (columns 2k and 2k + 1).
+using F8 = uint64_t[4];
+
+template <typename T>
+__device__ __forceinline__ void widen(const Raw<T>& r, F8& v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 4) {
+            v[k] = f2_pack(__uint_as_float(r.w[2 * k]), __uint_as_float(r.w[2 * k + 1]));
+        } else if constexpr (std::is_same<T, bf16>::value) {
+            v[k] = f2_pack(__uint_as_float(r.w[k] << 16), __uint_as_float(r.w[k] & 0xffff0000u));
+        } else {
+            const float2 f = h2x2_to_f2(r.w[k]);
+            v[k] = f2_pack(f.x, f.y);
+        }
+    }
+}
+
+// q*scale of the codes: the byte in the mantissa of 2^23, the bias 2^23 + 128 off, both exact.
+template <typename T>
+__device__ __forceinline__ void widen_codes(const Raw<T>& r, F8& v) {
+    const uint64_t bias = f2_pack(8388736.0f, 8388736.0f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t w = r.w[k / 2], j = 2 * (k & 1);
+        const float s = __uint_as_float(r.w[2 + k / 2]);
+        const uint64_t q = f2_pack(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540u + j)),
+                                   __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7541u + j)));
+        v[k] = f2_mul(f2_sub(q, bias), f2_pack(s, s));
+    }
+}
+
+// The row r of a matrix or of a checkpoint, and its values.
+template <typename T, bool kVec>
+__device__ __forceinline__ Raw<T> load_row(const Mat& m, const uint8_t* ck, const CkptShape& s,
+                                           uint64_t r, const Cols<kVec>& c) {
+    if (ck) return load_codes<T, kVec>(ck + r * s.row_bytes, s, c);
+    return load_raw<T, kVec>((const T*)m.p + r * m.ld, c);
+}
+
+template <typename T>
+__device__ __forceinline__ void widen_row(const Raw<T>& raw, bool codes, F8& v) {
+    if (codes)
+        widen_codes<T>(raw, v);
+    else
+        widen<T>(raw, v);
+}
+
+// A vector of cols values, or `none` everywhere.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_vec(const void* p, float none, const Cols<kVec>& c, F8& v) {
+    if (p) {
+        widen<T>(load_raw<T, kVec>((const T*)p, c), v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = f2_pack(none, none);
+    }
+}
+
+// Zero the columns that do not exist.
+template <bool kVec>
+__device__ __forceinline__ void clear_missing(const Cols<kVec>& c, F8& v) {
+    if (c.mask == 0xffu) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a, b;
+        f2_unpack(v[k], a, b);
+        v[k] = f2_pack(c.mask >> (2 * k) & 1u ? a : 0.0f, c.mask >> (2 * k + 1) & 1u ? b : 0.0f);
+    }
+}
+
+__device__ __forceinline__ float sum8(const F8& v) {
+    float a, b;
+    f2_unpack(f2_add(f2_add(v[0], v[1]), f2_add(v[2], v[3])), a, b);
+    return __fadd_rn(a, b);
+}
+
+__device__ __forceinline__ float dot8(const F8& x, const F8& y) {
+    uint64_t s = f2_mul(x[0], y[0]);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) s = f2_fma(x[k], y[k], s);
+    float a, b;
+    f2_unpack(s, a, b);
+    return __fadd_rn(a, b);
+}
+
+template <typename T>
+__device__ __forceinline__ Raw<T> narrow(const F8& v) {
+    Raw<T> r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a, b;
+        f2_unpack(v[k], a, b);
+        if constexpr (sizeof(T) == 4) {
+            r.w[2 * k] = __float_as_uint(a);
+            r.w[2 * k + 1] = __float_as_uint(b);
+        } else if constexpr (std::is_same<T, bf16>::value) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[k]) : "f"(b), "f"(a));
+        } else {
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r.w[k]) : "f"(b), "f"(a));
+        }
+    }
+    return r;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_raw(T* row, const Cols<kVec>& c, const Raw<T>& r) {
+    if (kVec && c.mask == 0xffu) {
+        uint4* p = reinterpret_cast<uint4*>(row + c.c0);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+            p[k] = make_uint4(r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (!(c.mask >> j & 1u)) continue;
+        if constexpr (sizeof(T) == 4)
+            reinterpret_cast<uint32_t*>(row)[c.at(j)] = r.w[j];
+        else
+            reinterpret_cast<uint16_t*>(row)[c.at(j)] = (uint16_t)(r.w[j / 2] >> 16 * (j & 1));
+    }
+}
+
+// Largest |x| of the lane's first and second four columns as binary32 bits. 16-bit magnitudes
+// order like integers: two at a time.
+template <typename T>
+__device__ __forceinline__ void lane_amax(const Raw<T>& r, uint32_t (&m)[2]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            m[k] = max(max(r.w[4 * k] & 0x7fffffffu, r.w[4 * k + 1] & 0x7fffffffu),
+                       max(r.w[4 * k + 2] & 0x7fffffffu, r.w[4 * k + 3] & 0x7fffffffu));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t h = __vmaxu2(r.w[2 * k] & 0x7fff7fffu, r.w[2 * k + 1] & 0x7fff7fffu);
+            m[k] = max(h & 0xffffu, h >> 16);
+        }
+    }
+}
+
+// The bits of the binary32 value of a magnitude that lane_amax gave.
+template <typename T>
+__device__ __forceinline__ uint32_t amax_bits(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    if constexpr (std::is_same<T, bf16>::value) return m << 16;
+    return __float_as_uint(h2f((uint16_t)m));
+}
+
+// The largest magnitude of each of the warp's two blocks, the same in every lane.
+template <typename T, bool kVec>
+__device__ __forceinline__ void block_amax(const Raw<T>& r, uint32_t lane, uint32_t (&a)[2]) {
+    uint32_t m[2];
+    lane_amax<T>(r, m);
+    if constexpr (kVec) {   // 16 lanes per block
+        m[0] = max(m[0], m[1]);
+        m[1] = lane < 16u ? 0u : m[0];
+        m[0] = lane < 16u ? m[0] : 0u;
+    }
+    a[0] = __reduce_max_sync(0xffffffffu, m[0]);
+    a[1] = __reduce_max_sync(0xffffffffu, m[1]);
+}
+
+// Write the codes and scales of a warp's 256 columns into a checkpoint row; every lane of the
+// warp calls it (missing columns hold zeros). scale, inv: of the lane's block (kVec), or of the
+// blocks of its first and second four columns.
+template <bool kVec>
+__device__ __forceinline__ void put_codes(uint8_t* row, const CkptShape& s, const Cols<kVec>& c,
+                                          uint32_t lane, const F8& v, const float (&scale)[2],
+                                          const float (&inv)[2]) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f2_unpack(v[k], x[2 * k], x[2 * k + 1]);
+    const uint32_t block = c.c0 >> 7;
+    if constexpr (kVec) {
+        if (c.c0 < s.code_bytes)
+            *reinterpret_cast<uint2*>(row + c.c0) = q8_codes(x, scale[0], inv[0]);
+        if ((lane & 15u) == 0 && block < s.blocks)
+            *reinterpret_cast<float*>(row + s.code_bytes + 4u * block) = scale[0];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = j < 4 ? x[4 * k + j] : 0.0f;
+            const uint32_t w = q8_codes(y, scale[k], inv[k]).x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c.at(4 * k + j) < s.code_bytes)
+                    row[c.at(4 * k + j)] = (uint8_t)(w >> 8 * j);
+            if (lane == 0 && block + k < s.blocks)
+                *reinterpret_cast<float*>(row + s.code_bytes + 4u * (block + k)) = scale[k];
+        }
+    }
+}
+
+// The same from values and their T (whose magnitudes give the scales).
+template <typename T, bool kVec>
+__device__ __forceinline__ void save_codes(uint8_t* row, const CkptShape& s, const Cols<kVec>& c,
+                                           uint32_t lane, const Raw<T>& raw, const F8& v) {
+    uint32_t a[2];
+    block_amax<T, kVec>(raw, lane, a);
+    if (kVec) a[0] = lane < 16u ? a[0] : a[1];
+    float scale[2], inv[2];
+    scale[0] = q8_scale(amax_bits<T>(a[0]));
+    inv[0] = __fdiv_rn(1.0f, scale[0]);
+    if (!kVec) {
+        scale[1] = q8_scale(amax_bits<T>(a[1]));
+        inv[1] = __fdiv_rn(1.0f, scale[1]);
+    }
+    put_codes<kVec>(row, s, c, lane, v, scale, inv);
+}
+
+// Zeros behind a row's scales (at most seven words).
+__device__ __forceinline__ void save_pad(uint8_t* row, const CkptShape& s, uint32_t lane) {
+    const uint64_t at = s.code_bytes + 4ull * s.blocks + 4ull * lane;
+    if (at < s.row_bytes) *reinterpret_cast<uint32_t*>(row + at) = 0u;
+}
+
 __device__ __forceinline__ void grid_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 __device__ __forceinline__ void grid_launch_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Whether a matrix's rows all start on a 16-byte boundary.
+template <typename T>
+bool rows_aligned(const Mat& m) {
+    return aligned16(m.p) && m.ld % (16 / sizeof(T)) == 0;
 }
 
 template <typename K, typename... A>

@@ -5,106 +5,174 @@
 // Per block of 128 columns of a row: scale = amax/127, q = round_half_even(x/scale), stored as
 // q + 128; an inf or NaN poisons the block (scale NaN, q 0). The read is T(q*scale).
 //
-// One warp per block and row: lane l holds columns 4l..4l+3 of the block.
+// Bound by HBM: each direction moves the values once and about half as many bytes of records
+// (fp16). A warp takes kN * 256 neighbouring columns of a row at a time and loads them all
+// before it works on the first: one address and one step per piece, and the two divisions that
+// the scales need once per piece (pieces of one chunk each, stepped separately, issued twice the
+// instructions, and the kernel was bound by them).
 #include "zero_act.cuh"
 
 namespace zk {
 namespace {
 
-template <typename T>
-__global__ void __launch_bounds__(256) ckpt_save_kernel(uint64_t rows, CkptShape s, const T* x,
-                                                        uint64_t ldx, uint8_t* ckpt) {
+constexpr int kThreads = 256;
+
+// The pieces of a matrix, row by row, and the step to the same warp's next piece.
+struct Pieces {
+    uint64_t rows;
+    uint32_t per_row;
+    uint32_t step_rows, step_pieces;   // warps of the grid = step_rows * per_row + step_pieces
+};
+
+struct Piece {
+    uint64_t row;
+    uint32_t at;
+    __device__ __forceinline__ void next(const Pieces& p) {
+        row += p.step_rows;
+        at += p.step_pieces;
+        if (at >= p.per_row) {
+            at -= p.per_row;
+            ++row;
+        }
+    }
+};
+
+__device__ __forceinline__ Piece first_piece(const Pieces& p) {
+    const uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    Piece a;
+    a.row = w / p.per_row;
+    a.at = (uint32_t)(w - a.row * p.per_row);
+    return a;
+}
+
+// Lane 2k + b divides for block b of chunk k.
+template <typename T, bool kVec, int kN>
+__global__ void __launch_bounds__(kThreads) ckpt_save_kernel(Pieces p, CkptShape s, Mat x,
+                                                             uint8_t* ckpt) {
     grid_wait();
-    const int lane = threadIdx.x & 31;
-    const uint64_t units = rows * s.blocks;
-    for (uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < units;
-         w += (uint64_t)gridDim.x * 8) {
-        const uint64_t r = w / s.blocks;
-        const uint32_t b = (uint32_t)(w - r * s.blocks);
-        const uint32_t c0 = b * 128u + lane * 4u;
-        float v[4];
-        uint32_t amax = 0;
-        for (int j = 0; j < 4; ++j) {
-            v[j] = c0 + j < s.cols ? to_f(x[r * ldx + c0 + j]) : 0.0f;
-            amax = max(amax, abs_bits(v[j]));
+    const uint32_t lane = threadIdx.x & 31;
+    for (Piece i = first_piece(p); i.row < p.rows; i.next(p)) {
+        const T* src = (const T*)x.p + i.row * x.ld;
+        uint8_t* row = ckpt + i.row * s.row_bytes;
+        Raw<T> raw[kN];
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+            raw[k] = load_raw<T, kVec>(src, Cols<kVec>(i.at * kN + k, lane, s.cols));
+        uint32_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            uint32_t a[2];
+            block_amax<T, kVec>(raw[k], lane, a);
+            if (lane == 2 * k) mine = a[0];
+            if (lane == 2 * k + 1) mine = a[1];
         }
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const float scale = q8_scale(amax);
-        uint8_t* row = ckpt + r * s.row_bytes;
-        if (c0 < s.code_bytes) {
-            uint32_t word = 0;
-            for (int j = 0; j < 4; ++j) word |= q8_code(v[j], scale) << (8 * j);
-            *reinterpret_cast<uint32_t*>(row + c0) = word;
+        const float scale = q8_scale(amax_bits<T>(mine)), inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            float sc[2], iv[2];
+            const int from = 2 * k + (kVec ? lane >> 4 : 0);
+            sc[0] = __shfl_sync(0xffffffffu, scale, from);
+            iv[0] = __shfl_sync(0xffffffffu, inv, from);
+            if (!kVec) {
+                sc[1] = __shfl_sync(0xffffffffu, scale, from + 1);
+                iv[1] = __shfl_sync(0xffffffffu, inv, from + 1);
+            }
+            F8 v;
+            widen<T>(raw[k], v);
+            put_codes<kVec>(row, s, Cols<kVec>(i.at * kN + k, lane, s.cols), lane, v, sc, iv);
         }
-        if (lane == 0) *reinterpret_cast<float*>(row + s.code_bytes + 4u * b) = scale;
-        if (b + 1 == s.blocks) {   // zeros behind the scales
-            const uint64_t at = s.code_bytes + 4ull * s.blocks + 4ull * lane;
-            if (at < s.row_bytes) *reinterpret_cast<uint32_t*>(row + at) = 0u;
+        if (i.at == 0) save_pad(row, s, lane);
+    }
+}
+
+template <typename T, bool kVec, int kN>
+__global__ void __launch_bounds__(kThreads) ckpt_load_kernel(Pieces p, CkptShape s,
+                                                             const uint8_t* ckpt, Mat y) {
+    grid_wait();
+    const uint32_t lane = threadIdx.x & 31;
+    for (Piece i = first_piece(p); i.row < p.rows; i.next(p)) {
+        const uint8_t* row = ckpt + i.row * s.row_bytes;
+        T* dst = (T*)y.p + i.row * y.ld;
+        Raw<T> raw[kN];
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+            raw[k] = load_codes<T, kVec>(row, s, Cols<kVec>(i.at * kN + k, lane, s.cols));
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            F8 v;
+            widen_codes<T>(raw[k], v);
+            store_raw<T, kVec>(dst, Cols<kVec>(i.at * kN + k, lane, s.cols), narrow<T>(v));
         }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) ckpt_load_kernel(uint64_t rows, CkptShape s,
-                                                        const uint8_t* ckpt, T* out,
-                                                        uint64_t ldo) {
-    grid_wait();
-    const int lane = threadIdx.x & 31;
-    const uint64_t units = rows * s.blocks;
-    for (uint64_t w = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < units;
-         w += (uint64_t)gridDim.x * 8) {
-        const uint64_t r = w / s.blocks;
-        const uint32_t b = (uint32_t)(w - r * s.blocks);
-        const uint32_t c0 = b * 128u + lane * 4u;
-        const uint8_t* row = ckpt + r * s.row_bytes;
-        if (c0 >= s.cols) continue;
-        const float scale = ckpt_scales(row, s)[b];
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(row + c0);
-        for (int j = 0; j < 4; ++j)
-            if (c0 + j < s.cols)
-                out[r * ldo + c0 + j] = from_f<T>(q8_value(word >> (8 * j) & 255u, scale));
-    }
+// As many warps as pieces, at most kWaves CTAs per SM.
+constexpr int kWaves = 16;
+
+// Chunks per piece: four, unless a row is shorter or would leave most of a piece unused.
+int chunks_per_piece(uint32_t cols) {
+    const uint32_t chunks = (cols + kWarpCols - 1) / kWarpCols;
+    return chunks >= 3 ? 4 : (int)chunks;
 }
 
-cudaError_t unit_grid(uint64_t units, unsigned* grid) {
+cudaError_t split(uint64_t rows, const CkptShape& s, int n, Pieces* p, unsigned* grid) {
     DevInfo di;
     const cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
-    const uint64_t blocks = (units + 7) / 8, cap = (uint64_t)di.sms * 8;
+    p->rows = rows;
+    p->per_row = (s.cols + n * kWarpCols - 1) / (n * kWarpCols);
+    const uint64_t warps = kThreads / 32;
+    const uint64_t blocks = (rows * p->per_row + warps - 1) / warps;
+    const uint64_t cap = (uint64_t)di.sms * kWaves;
     *grid = (unsigned)(blocks < cap ? blocks : cap);
+    const uint64_t step = *grid * warps;
+    p->step_rows = (uint32_t)(step / p->per_row);
+    p->step_pieces = (uint32_t)(step % p->per_row);
     return cudaSuccess;
+}
+
+template <typename T, int kN>
+cudaError_t run(bool save, uint64_t rows, const CkptShape& s, const Mat& m, uint8_t* ckpt,
+                cudaStream_t stream) {
+    Pieces p;
+    unsigned grid = 1;
+    const cudaError_t e = split(rows, s, kN, &p, &grid);
+    if (e != cudaSuccess) return e;
+    const bool vec = rows_aligned<T>(m);
+    if (save)
+        return launch_act(vec ? ckpt_save_kernel<T, true, kN> : ckpt_save_kernel<T, false, kN>,
+                          dim3(grid), kThreads, 0, stream, p, s, m, ckpt);
+    return launch_act(vec ? ckpt_load_kernel<T, true, kN> : ckpt_load_kernel<T, false, kN>,
+                      dim3(grid), kThreads, 0, stream, p, s, (const uint8_t*)ckpt, m);
+}
+
+template <typename T>
+cudaError_t run_t(bool save, uint64_t rows, const CkptShape& s, const Mat& m, uint8_t* ckpt,
+                  cudaStream_t stream) {
+    switch (chunks_per_piece(s.cols)) {
+        case 1: return run<T, 1>(save, rows, s, m, ckpt, stream);
+        case 2: return run<T, 2>(save, rows, s, m, ckpt, stream);
+        default: return run<T, 4>(save, rows, s, m, ckpt, stream);
+    }
+}
+
+cudaError_t run_any(bool save, uint64_t rows, const CkptShape& s, int dtype, const Mat& m,
+                    uint8_t* ckpt, cudaStream_t stream) {
+    return dtype == ZERO_F16    ? run_t<__half>(save, rows, s, m, ckpt, stream)
+           : dtype == ZERO_BF16 ? run_t<bf16>(save, rows, s, m, ckpt, stream)
+                                : run_t<float>(save, rows, s, m, ckpt, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_save(uint64_t rows, const CkptShape& s, int dtype, const Mat& x,
                              uint8_t* ckpt, cudaStream_t stream) {
-    unsigned grid = 1;
-    const cudaError_t e = unit_grid(rows * s.blocks, &grid);
-    if (e != cudaSuccess) return e;
-    if (dtype == ZERO_F16)
-        return launch_act(ckpt_save_kernel<__half>, dim3(grid), 256, 0, stream, rows, s,
-                          (const __half*)x.p, x.ld, ckpt);
-    if (dtype == ZERO_BF16)
-        return launch_act(ckpt_save_kernel<bf16>, dim3(grid), 256, 0, stream, rows, s,
-                          (const bf16*)x.p, x.ld, ckpt);
-    return launch_act(ckpt_save_kernel<float>, dim3(grid), 256, 0, stream, rows, s,
-                      (const float*)x.p, x.ld, ckpt);
+    return run_any(true, rows, s, dtype, x, ckpt, stream);
 }
 
 cudaError_t launch_ckpt_load(uint64_t rows, const CkptShape& s, int dtype, const uint8_t* ckpt,
                              const Mat& out, cudaStream_t stream) {
-    unsigned grid = 1;
-    const cudaError_t e = unit_grid(rows * s.blocks, &grid);
-    if (e != cudaSuccess) return e;
-    if (dtype == ZERO_F16)
-        return launch_act(ckpt_load_kernel<__half>, dim3(grid), 256, 0, stream, rows, s, ckpt,
-                          (__half*)out.p, out.ld);
-    if (dtype == ZERO_BF16)
-        return launch_act(ckpt_load_kernel<bf16>, dim3(grid), 256, 0, stream, rows, s, ckpt,
-                          (bf16*)out.p, out.ld);
-    return launch_act(ckpt_load_kernel<float>, dim3(grid), 256, 0, stream, rows, s, ckpt,
-                      (float*)out.p, out.ld);
+    return run_any(false, rows, s, dtype, out, const_cast<uint8_t*>(ckpt), stream);
 }
 
 }  // namespace zk
