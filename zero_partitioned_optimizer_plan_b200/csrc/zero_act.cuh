@@ -58,42 +58,82 @@ __device__ __forceinline__ uint32_t q8_code(float x, float scale) {
 // least 2^-100 the quotients stay below 127.5, and 1/scale lies strictly between inv*(1 - 2^-21)
 // and inv*(1 + 2^-21), wide enough that fl(x/scale) lies between the two products too: where
 // both products round to the same integer, fl(x/scale) rounds to it. (Rounding: the fused
-// multiply-add into 1.5 * 2^23 + 128 leaves the integer + 128 in the low byte.) The others, and
-// smaller, zero or NaN scales, take the division.
+// multiply-add into 1.5 * 2^23 + 128 leaves the integer + 128 in the low byte.) The others are
+// settled by q8_near, and smaller, zero or NaN scales by division.
 constexpr float kQ8Bias = 12583040.0f;
 
-__device__ __noinline__ uint2 q8_codes_by_division(const float4 a, const float4 b, float scale) {
-    return make_uint2(q8_code(a.x, scale) | q8_code(a.y, scale) << 8 | q8_code(a.z, scale) << 16 |
-                          q8_code(a.w, scale) << 24,
-                      q8_code(b.x, scale) | q8_code(b.y, scale) << 8 | q8_code(b.z, scale) << 16 |
-                          q8_code(b.w, scale) << 24);
+// Eight integers + 128, as they lie in the low bytes of kQ8Bias + integer, packed.
+__device__ __forceinline__ uint2 q8_bytes(const float (&c)[8]) {
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t p = __byte_perm(__float_as_uint(c[4 * k]), __float_as_uint(c[4 * k + 1]), 0x0040u);
+        const uint32_t q = __byte_perm(__float_as_uint(c[4 * k + 2]), __float_as_uint(c[4 * k + 3]), 0x0040u);
+        w[k] = __byte_perm(p, q, 0x5410u);
+    }
+    return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ uint2 q8_codes(const float (&x)[8], float scale, float inv) {
+// The first four values have scale s0, the others s1 (one and the same, or two). Returns false
+// if some value needs q8_codes_near.
+__device__ __forceinline__ bool q8_codes(const float (&x)[8], float s0, float s1, float inv0,
+                                         float inv1, uint2& out) {
     float c[8];
     uint32_t differ = 0;
-    const float lo = __fmul_rn(inv, 1.0f - 0x1p-21f), hi = __fmul_rn(inv, 1.0f + 0x1p-21f);
-    const uint64_t l2 = f2_pack(lo, lo), h2 = f2_pack(hi, hi), bias = f2_pack(kQ8Bias, kQ8Bias);
+    const uint64_t bias = f2_pack(kQ8Bias, kQ8Bias);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-        const uint64_t v = f2_pack(x[j], x[j + 1]);
+        const float inv = j < 4 ? inv0 : inv1;
+        const float lo = __fmul_rn(inv, 1.0f - 0x1p-21f), hi = __fmul_rn(inv, 1.0f + 0x1p-21f);
+        const uint64_t v = f2_pack(x[j], x[j + 1]), l2 = f2_pack(lo, lo), h2 = f2_pack(hi, hi);
         float a, b;
         f2_unpack(f2_fma(v, l2, bias), a, b);
         f2_unpack(f2_fma(v, h2, bias), c[j], c[j + 1]);
         differ |= __float_as_uint(a) ^ __float_as_uint(c[j]);
         differ |= __float_as_uint(b) ^ __float_as_uint(c[j + 1]);
     }
-    if (!(scale >= 0x1p-100f) || differ != 0)
+    out = q8_bytes(c);
+    return differ == 0 && s0 >= 0x1p-100f && s1 >= 0x1p-100f;
+}
+
+// The integer nearest fl(x/scale), ties to even, as kQ8Bias + integer, where x/scale lies close
+// to m, halfway between the integers that the two products a and b rounded to. e = x - m*scale
+// is exact (18 bits), and fl(x/scale) is above, at or below m as e is above, within or below
+// half a unit in the last place of m times the scale. (At m = 1/2 the places below are narrower,
+// but there both answers round to 0.) No division: 16-bit values meet ties often, x = amax/2
+// among them.
+__device__ __forceinline__ float q8_near(float x, float scale, float a, float b) {
+    const float k0 = fminf(a, b), k1 = fmaxf(a, b);
+    const float m = __fadd_rn(__fsub_rn(k0, kQ8Bias), 0.5f);
+    const float e = __fmaf_rn(-m, scale, x);
+    const float half = __fmul_rn(__uint_as_float(__float_as_uint(m) & 0x7f800000u),
+                                 __fmul_rn(scale, 0x1p-24f));
+    const float even = (__float_as_uint(k0) & 1u) ? k1 : k0;
+    return a == b ? a : e > half ? k1 : e < -half ? k0 : even;
+}
+
+__device__ __noinline__ uint2 q8_codes_by_division(float4 a, float4 b, float s0, float s1) {
+    return make_uint2(q8_code(a.x, s0) | q8_code(a.y, s0) << 8 | q8_code(a.z, s0) << 16 |
+                          q8_code(a.w, s0) << 24,
+                      q8_code(b.x, s1) | q8_code(b.y, s1) << 8 | q8_code(b.z, s1) << 16 |
+                          q8_code(b.w, s1) << 24);
+}
+
+// The codes where q8_codes returned false.
+__device__ __forceinline__ uint2 q8_codes_near(const float (&x)[8], float s0, float s1, float inv0,
+                                               float inv1) {
+    if (!(s0 >= 0x1p-100f) || !(s1 >= 0x1p-100f))
         return q8_codes_by_division(make_float4(x[0], x[1], x[2], x[3]),
-                                    make_float4(x[4], x[5], x[6], x[7]), scale);
-    uint32_t w[2];
+                                    make_float4(x[4], x[5], x[6], x[7]), s0, s1);
+    float c[8];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t lo = __byte_perm(__float_as_uint(c[4 * k]), __float_as_uint(c[4 * k + 1]), 0x0040u);
-        const uint32_t hi = __byte_perm(__float_as_uint(c[4 * k + 2]), __float_as_uint(c[4 * k + 3]), 0x0040u);
-        w[k] = __byte_perm(lo, hi, 0x5410u);
+    for (int j = 0; j < 8; ++j) {
+        const float inv = j < 4 ? inv0 : inv1;
+        c[j] = q8_near(x[j], j < 4 ? s0 : s1,
+                       __fmaf_rn(x[j], __fmul_rn(inv, 1.0f - 0x1p-21f), kQ8Bias),
+                       __fmaf_rn(x[j], __fmul_rn(inv, 1.0f + 0x1p-21f), kQ8Bias));
     }
-    return make_uint2(w[0], w[1]);
+    return q8_bytes(c);
 }
 
 __device__ __forceinline__ float q8_value(uint32_t byte, float scale) {
@@ -310,20 +350,38 @@ __device__ __forceinline__ void store_raw(T* row, const Cols<kVec>& c, const Raw
     }
 }
 
-// Largest |x| of the lane's first and second four columns as binary32 bits. 16-bit magnitudes
-// order like integers: two at a time.
+// Larger magnitude of each half (a NaN stays one); the sign bits of the result mean nothing.
 template <typename T>
+__device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (std::is_same<T, bf16>::value)
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Bits of T of the largest magnitude in a word of two (they order like the values).
+__device__ __forceinline__ uint32_t amax1(uint32_t h) {
+    return max(h & 0x7fffu, h >> 16 & 0x7fffu);
+}
+
+// Largest magnitude of the lane's first and second four columns, or (kVec) of all in m[0].
+template <typename T, bool kVec>
 __device__ __forceinline__ void lane_amax(const Raw<T>& r, uint32_t (&m)[2]) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             m[k] = max(max(r.w[4 * k] & 0x7fffffffu, r.w[4 * k + 1] & 0x7fffffffu),
                        max(r.w[4 * k + 2] & 0x7fffffffu, r.w[4 * k + 3] & 0x7fffffffu));
+        if (kVec) m[0] = max(m[0], m[1]);
     } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t h = __vmaxu2(r.w[2 * k] & 0x7fff7fffu, r.w[2 * k + 1] & 0x7fff7fffu);
-            m[k] = max(h & 0xffffu, h >> 16);
+        const uint32_t a = amax2<T>(r.w[0], r.w[1]), b = amax2<T>(r.w[2], r.w[3]);
+        if constexpr (kVec) {
+            m[0] = amax1(amax2<T>(a, b));
+        } else {
+            m[0] = amax1(a);
+            m[1] = amax1(b);
         }
     }
 }
@@ -340,9 +398,8 @@ __device__ __forceinline__ uint32_t amax_bits(uint32_t m) {
 template <typename T, bool kVec>
 __device__ __forceinline__ void block_amax(const Raw<T>& r, uint32_t lane, uint32_t (&a)[2]) {
     uint32_t m[2];
-    lane_amax<T>(r, m);
+    lane_amax<T, kVec>(r, m);
     if constexpr (kVec) {   // 16 lanes per block
-        m[0] = max(m[0], m[1]);
         m[1] = lane < 16u ? 0u : m[0];
         m[0] = lane < 16u ? m[0] : 0u;
     }
@@ -350,54 +407,90 @@ __device__ __forceinline__ void block_amax(const Raw<T>& r, uint32_t lane, uint3
     a[1] = __reduce_max_sync(0xffffffffu, m[1]);
 }
 
-// Write the codes and scales of a warp's 256 columns into a checkpoint row; every lane of the
-// warp calls it (missing columns hold zeros). scale, inv: of the lane's block (kVec), or of the
-// blocks of its first and second four columns.
-template <bool kVec>
-__device__ __forceinline__ void put_codes(uint8_t* row, const CkptShape& s, const Cols<kVec>& c,
-                                          uint32_t lane, const F8& v, const float (&scale)[2],
-                                          const float (&inv)[2]) {
-    float x[8];
+// The code words of N chunks of a warp; every value first takes the short way, so that
+// the chunks' instructions interleave and one branch covers them all. scale, inv: of the lane's
+// block (kVec), or of the blocks of its first and second four columns.
+template <typename T, bool kVec, int N>
+__device__ __forceinline__ void make_codes(const Raw<T> (&raw)[N], const float (&scale)[N][2],
+                                           const float (&inv)[N][2], uint2 (&w)[N]) {
+    bool fine[N];
+    bool all = true;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f2_unpack(v[k], x[2 * k], x[2 * k + 1]);
+    for (int k = 0; k < N; ++k) {
+        float x[8];
+        F8 v;
+        widen<T>(raw[k], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f2_unpack(v[j], x[2 * j], x[2 * j + 1]);
+        fine[k] = q8_codes(x, scale[k][0], scale[k][!kVec], inv[k][0], inv[k][!kVec], w[k]);
+        all = all && fine[k];
+    }
+    if (all) return;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (fine[k]) continue;
+        float x[8];
+        F8 v;
+        widen<T>(raw[k], v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f2_unpack(v[j], x[2 * j], x[2 * j + 1]);
+        w[k] = q8_codes_near(x, scale[k][0], scale[k][!kVec], inv[k][0], inv[k][!kVec]);
+    }
+}
+
+// Write a chunk's codes and scales into a checkpoint row.
+template <bool kVec>
+__device__ __forceinline__ void store_codes(uint8_t* row, const CkptShape& s, const Cols<kVec>& c,
+                                            uint32_t lane, uint2 w, const float (&scale)[2]) {
     const uint32_t block = c.c0 >> 7;
     if constexpr (kVec) {
-        if (c.c0 < s.code_bytes)
-            *reinterpret_cast<uint2*>(row + c.c0) = q8_codes(x, scale[0], inv[0]);
+        if (c.c0 < s.code_bytes) *reinterpret_cast<uint2*>(row + c.c0) = w;
         if ((lane & 15u) == 0 && block < s.blocks)
             *reinterpret_cast<float*>(row + s.code_bytes + 4u * block) = scale[0];
     } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float y[8];
+        for (int j = 0; j < 8; ++j)
+            if (c.at(j) < s.code_bytes)
+                row[c.at(j)] = (uint8_t)((j < 4 ? w.x : w.y) >> 8 * (j & 3));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = j < 4 ? x[4 * k + j] : 0.0f;
-            const uint32_t w = q8_codes(y, scale[k], inv[k]).x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c.at(4 * k + j) < s.code_bytes)
-                    row[c.at(4 * k + j)] = (uint8_t)(w >> 8 * j);
+        for (int k = 0; k < 2; ++k)
             if (lane == 0 && block + k < s.blocks)
                 *reinterpret_cast<float*>(row + s.code_bytes + 4u * (block + k)) = scale[k];
-        }
     }
 }
 
-// The same from values and their T (whose magnitudes give the scales).
-template <typename T, bool kVec>
-__device__ __forceinline__ void save_codes(uint8_t* row, const CkptShape& s, const Cols<kVec>& c,
-                                           uint32_t lane, const Raw<T>& raw, const F8& v) {
-    uint32_t a[2];
-    block_amax<T, kVec>(raw, lane, a);
-    if (kVec) a[0] = lane < 16u ? a[0] : a[1];
-    float scale[2], inv[2];
-    scale[0] = q8_scale(amax_bits<T>(a[0]));
-    inv[0] = __fdiv_rn(1.0f, scale[0]);
-    if (!kVec) {
-        scale[1] = q8_scale(amax_bits<T>(a[1]));
-        inv[1] = __fdiv_rn(1.0f, scale[1]);
+// Codes and scales of N chunks of a row, the chunks of `at` .. (missing columns hold zeros);
+// every lane of the warp calls it. Lane 2k + b divides for block b of chunk k: two divisions for
+// all the scales and their reciprocals.
+template <typename T, bool kVec, int N>
+__device__ __forceinline__ void save_chunks(uint8_t* row, const CkptShape& s, uint32_t at,
+                                            uint32_t stride, uint32_t lane,
+                                            const Raw<T> (&raw)[N]) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        uint32_t a[2];
+        block_amax<T, kVec>(raw[k], lane, a);
+        if (lane == 2 * k) mine = a[0];
+        if (lane == 2 * k + 1) mine = a[1];
     }
-    put_codes<kVec>(row, s, c, lane, v, scale, inv);
+    const float own = q8_scale(amax_bits<T>(mine)), own_inv = __fdiv_rn(1.0f, own);
+    float scale[N][2], inv[N][2];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int from = 2 * k + (kVec ? lane >> 4 : 0);
+        scale[k][0] = __shfl_sync(0xffffffffu, own, from);
+        inv[k][0] = __shfl_sync(0xffffffffu, own_inv, from);
+        if (!kVec) {
+            scale[k][1] = __shfl_sync(0xffffffffu, own, from + 1);
+            inv[k][1] = __shfl_sync(0xffffffffu, own_inv, from + 1);
+        }
+    }
+    uint2 w[N];
+    make_codes<T, kVec, N>(raw, scale, inv, w);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        store_codes<kVec>(row, s, Cols<kVec>(at + k * stride, lane, s.cols), lane, w[k], scale[k]);
 }
 
 // Zeros behind a row's scales (at most seven words).

@@ -45,10 +45,9 @@ __device__ __forceinline__ Piece first_piece(const Pieces& p) {
     return a;
 }
 
-// Lane 2k + b divides for block b of chunk k.
 template <typename T, bool kVec, int kN>
-__global__ void __launch_bounds__(kThreads) ckpt_save_kernel(Pieces p, CkptShape s, Mat x,
-                                                             uint8_t* ckpt) {
+__global__ void __launch_bounds__(kThreads, 4)
+    ckpt_save_kernel(Pieces p, CkptShape s, Mat x, uint8_t* ckpt) {
     grid_wait();
     const uint32_t lane = threadIdx.x & 31;
     for (Piece i = first_piece(p); i.row < p.rows; i.next(p)) {
@@ -58,29 +57,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(Pieces p, CkptShape
 #pragma unroll
         for (int k = 0; k < kN; ++k)
             raw[k] = load_raw<T, kVec>(src, Cols<kVec>(i.at * kN + k, lane, s.cols));
-        uint32_t mine = 0;
-#pragma unroll
-        for (int k = 0; k < kN; ++k) {
-            uint32_t a[2];
-            block_amax<T, kVec>(raw[k], lane, a);
-            if (lane == 2 * k) mine = a[0];
-            if (lane == 2 * k + 1) mine = a[1];
-        }
-        const float scale = q8_scale(amax_bits<T>(mine)), inv = __fdiv_rn(1.0f, scale);
-#pragma unroll
-        for (int k = 0; k < kN; ++k) {
-            float sc[2], iv[2];
-            const int from = 2 * k + (kVec ? lane >> 4 : 0);
-            sc[0] = __shfl_sync(0xffffffffu, scale, from);
-            iv[0] = __shfl_sync(0xffffffffu, inv, from);
-            if (!kVec) {
-                sc[1] = __shfl_sync(0xffffffffu, scale, from + 1);
-                iv[1] = __shfl_sync(0xffffffffu, inv, from + 1);
-            }
-            F8 v;
-            widen<T>(raw[k], v);
-            put_codes<kVec>(row, s, Cols<kVec>(i.at * kN + k, lane, s.cols), lane, v, sc, iv);
-        }
+        save_chunks<T, kVec, kN>(row, s, i.at * kN, 1, lane, raw);
         if (i.at == 0) save_pad(row, s, lane);
     }
 }
