@@ -15,7 +15,7 @@
 namespace zk {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // The pieces of a matrix, row by row, and the step to the same warp's next piece.
 struct Pieces {
@@ -46,7 +46,7 @@ __device__ __forceinline__ Piece first_piece(const Pieces& p) {
 }
 
 template <typename T, bool kVec, int kN>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kVec && sizeof(T) == 2 ? 7 : 6)
     ckpt_save_kernel(Pieces p, CkptShape s, Mat x, uint8_t* ckpt) {
     grid_wait();
     const uint32_t lane = threadIdx.x & 31;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(Pieces p, CkptShape
 }
 
 // As many warps as pieces, at most kWaves CTAs per SM.
-constexpr int kWaves = 16;
+constexpr int kWaves = 32;
 
 // Chunks per piece: four, unless a row is shorter or would leave most of a piece unused.
 int chunks_per_piece(uint32_t cols) {
