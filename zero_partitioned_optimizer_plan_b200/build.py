@@ -10,6 +10,7 @@ _build/ptxas.log.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import shutil
@@ -54,13 +55,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
     objs = []
     ptxas_log = []
-    for src in _sources():
+
+    def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         if src.endswith(".cu"):
             cmd = [NVCC, *NVCC_FLAGS, "-c", src, "-o", obj]
         else:
             cmd = ["g++", *CXX_FLAGS, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        return src, obj, cmd, subprocess.run(cmd, capture_output=True, text=True)
+
+    # the sources are independent: one compiler per core at most
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        done = list(pool.map(compile_one, _sources()))
+    for src, obj, cmd, r in done:
         if r.returncode != 0:
             raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if src.endswith(".cu"):

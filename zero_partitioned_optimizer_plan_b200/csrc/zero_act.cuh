@@ -46,20 +46,12 @@ __device__ __forceinline__ float q8_scale(uint32_t amax) {
                                : __fdiv_rn(__uint_as_float(amax), 127.0f);
 }
 
-// Code byte of x by division. A scale of 0 or NaN gives q = 0. The quotient of a subnormal scale
-// can pass 127 (the scale itself was rounded): clamped.
-__device__ __forceinline__ uint32_t q8_code(float x, float scale) {
-    if (!(scale > 0.0f)) return 128u;
-    const int q = __float2int_rn(__fdiv_rn(x, scale));
-    return (uint32_t)(min(max(q, -127), 127) + 128);
-}
-
 // The code bytes of the values x[0..7], as two words, from inv = fl(1/scale). For a scale of at
 // least 2^-100 the quotients stay below 127.5, and 1/scale lies strictly between inv*(1 - 2^-21)
 // and inv*(1 + 2^-21), wide enough that fl(x/scale) lies between the two products too: where
 // both products round to the same integer, fl(x/scale) rounds to it. (Rounding: the fused
-// multiply-add into 1.5 * 2^23 + 128 leaves the integer + 128 in the low byte.) The others are
-// settled by q8_near, and smaller, zero or NaN scales by division.
+// multiply-add into 1.5 * 2^23 + 128 leaves the integer + 128 in the low byte.) The others,
+// and smaller, zero or NaN scales, take q8_codes_near.
 constexpr float kQ8Bias = 12583040.0f;
 
 // Eight integers + 128, as they lie in the low bytes of kQ8Bias + integer, packed.
@@ -112,26 +104,27 @@ __device__ __forceinline__ float q8_near(float x, float scale, float a, float b)
     return a == b ? a : e > half ? k1 : e < -half ? k0 : even;
 }
 
-__device__ __noinline__ uint2 q8_codes_by_division(float4 a, float4 b, float s0, float s1) {
-    return make_uint2(q8_code(a.x, s0) | q8_code(a.y, s0) << 8 | q8_code(a.z, s0) << 16 |
-                          q8_code(a.w, s0) << 24,
-                      q8_code(b.x, s1) | q8_code(b.y, s1) << 8 | q8_code(b.z, s1) << 16 |
-                          q8_code(b.w, s1) << 24);
-}
-
-// The codes where q8_codes returned false.
+// The codes where q8_codes returned false. A small scale is first multiplied by 2^80, and the
+// values with it (exact, and the quotients stay); it may have been rounded by up to half of
+// itself, so the codes are clamped. A scale of 0 or NaN gives q = 0.
 __device__ __forceinline__ uint2 q8_codes_near(const float (&x)[8], float s0, float s1, float inv0,
                                                float inv1) {
-    if (!(s0 >= 0x1p-100f) || !(s1 >= 0x1p-100f))
-        return q8_codes_by_division(make_float4(x[0], x[1], x[2], x[3]),
-                                    make_float4(x[4], x[5], x[6], x[7]), s0, s1);
+    const float s[2] = {s0, s1};
+    const float inv[2] = {inv0, inv1};
     float c[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float inv = j < 4 ? inv0 : inv1;
-        c[j] = q8_near(x[j], j < 4 ? s0 : s1,
-                       __fmaf_rn(x[j], __fmul_rn(inv, 1.0f - 0x1p-21f), kQ8Bias),
-                       __fmaf_rn(x[j], __fmul_rn(inv, 1.0f + 0x1p-21f), kQ8Bias));
+    for (int h = 0; h < 2; ++h) {
+        const bool normal = s[h] >= 0x1p-100f, any = s[h] > 0.0f;
+        const float up = normal ? 1.0f : any ? 0x1p80f : 0.0f;
+        const float scale = normal ? s[h] : any ? __fmul_rn(s[h], 0x1p80f) : 1.0f;
+        const float r = normal ? inv[h] : __fdiv_rn(1.0f, scale);
+        const float lo = __fmul_rn(r, 1.0f - 0x1p-21f), hi = __fmul_rn(r, 1.0f + 0x1p-21f);
+#pragma unroll
+        for (int j = 4 * h; j < 4 * h + 4; ++j) {
+            const float v = any ? __fmul_rn(x[j], up) : 0.0f;
+            c[j] = q8_near(v, scale, __fmaf_rn(v, lo, kQ8Bias), __fmaf_rn(v, hi, kQ8Bias));
+            c[j] = fminf(fmaxf(c[j], kQ8Bias - 127.0f), kQ8Bias + 127.0f);
+        }
     }
     return q8_bytes(c);
 }
@@ -155,6 +148,7 @@ template <bool kVec>
 struct Cols {
     uint32_t c0, cols;
     uint32_t mask;   // bit j: column j exists
+    __device__ __forceinline__ Cols() : c0(0), cols(0), mask(0) {}
     __device__ __forceinline__ Cols(uint32_t chunk, uint32_t lane, uint32_t n) : cols(n), mask(0) {
         c0 = chunk * kWarpCols + (kVec ? 8u * lane : lane);
         const uint32_t left = n > c0 ? n - c0 : 0u;

@@ -1,306 +1,223 @@
-// The block boundary for sm_100a: y = rs*x + bs*gate*post(h), u = pre(y), and its gradient.
+// The block boundary for sm_100a: y = rs*x + bs*gate*post(h), u = pre(y), and the 8-bit
+// checkpoints of y and h.
 //
-// One CTA per row; the row is read again in each pass (statistics of h, of y, the outputs), from
-// the L1 cache. The vector gradients are summed by a second kernel, one CTA per 32 columns, from
-// row statistics that the first one leaves in the workspace.
-#include "zero_act.cuh"
+// Bound by HBM: every matrix is read or written once. Eight columns per lane and 256 per warp
+// stay in registers from the load to the last use; the sums over a row go through warp shuffles
+// and, where several warps share a row (a "team"), one exchange through shared memory each.
+//
+// A norm's statistics need one sum for RMS (of z^2) and two in turn for LayerNorm (of z, then of
+// (z - mean)^2: the difference of large squares would lose the variance of a row with a mean).
+#include "zero_join.cuh"
 
 namespace zk {
-
-constexpr int kRowStats = 6;   // mean, 1/deviation of h; of y; the two means of pre's gradient
-
-uint64_t join_workspace(uint64_t rows, uint64_t cols, uint64_t) {
-    return cols ? (rows * kRowStats * 4 + 15) / 16 * 16 : 0;
-}
-
 namespace {
 
-constexpr int kThreads = 256;
-
-template <typename T>
-__device__ __forceinline__ float read_at(const Mat& m, const uint8_t* ck, const CkptShape& s,
-                                         uint64_t r, uint32_t c) {
-    if (ck) {
-        const uint8_t* row = ck + r * s.row_bytes;
-        return q8_value(row[c], ckpt_scales(row, s)[c / 128]);
-    }
-    return to_f(((const T*)m.p)[r * m.ld + c]);
-}
-
-template <typename T>
-__device__ __forceinline__ float vec_at(const void* v, uint32_t c, float none) {
-    return v ? to_f(((const T*)v)[c]) : none;
-}
-
-// Sum over the CTA, the same value in every thread, in a fixed order.
-__device__ __forceinline__ float cta_sum(float v) {
-    __shared__ float part[kThreads / 32];
-    for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, d));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.0f;
-    for (int i = 0; i < kThreads / 32; ++i) s = __fadd_rn(s, part[i]);
-    return s;
-}
-
-// Mean and 1/deviation of a row given by f(c).
-template <typename F>
-__device__ __forceinline__ void row_stats(int kind, uint32_t cols, float eps, F f, float* mean,
-                                          float* rstd) {
-    *mean = 0.0f;
-    *rstd = 1.0f;
-    if (kind == ZERO_NORM_NONE) return;
+// ---------------------------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------------------------
+// z - mean (LayerNorm; missing columns stay 0) and 1/deviation of the team's row.
+template <bool kVec, int G>
+__device__ __forceinline__ float centre(Team& t, int kind, float eps, float inv_cols,
+                                        const Cols<kVec> (&c)[G], F8 (&z)[G]) {
+    float s[2];
     if (kind == ZERO_NORM_LAYER) {
-        float s = 0.0f;
-        for (uint32_t c = threadIdx.x; c < cols; c += kThreads) s = __fadd_rn(s, f(c));
-        *mean = __fdiv_rn(cta_sum(s), (float)cols);
+        s[0] = s[1] = 0.0f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) s[0] = __fadd_rn(s[0], sum8(z[g]));
+        team_sum<2>(t, s);
+        const uint64_t m = both(__fmul_rn(s[0], -inv_cols));
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[g][k] = f2_add(z[g][k], m);
+            clear_missing<kVec>(c[g], z[g]);
+        }
     }
-    float q = 0.0f;
-    for (uint32_t c = threadIdx.x; c < cols; c += kThreads) {
-        const float d = __fsub_rn(f(c), *mean);
-        q = __fmaf_rn(d, d, q);
-    }
-    *rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(cta_sum(q), (float)cols), eps)));
+    s[0] = s[1] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) s[0] = __fadd_rn(s[0], dot8(z[g], z[g]));
+    team_sum<2>(t, s);
+    return __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], inv_cols), eps));
 }
 
-template <typename T>
-__device__ void save_row(uint8_t* ck, const CkptShape& s, uint64_t r, const T* v) {
-    const int lane = threadIdx.x & 31;
-    uint8_t* row = ck + r * s.row_bytes;
-    for (uint32_t b = threadIdx.x >> 5; b < s.blocks; b += kThreads / 32) {
-        float f[4];
-        uint32_t amax = 0;
-        const uint32_t c0 = b * 128u + lane * 4u;
-        for (int j = 0; j < 4; ++j) {
-            f[j] = c0 + j < s.cols ? to_f(v[c0 + j]) : 0.0f;
-            amax = max(amax, abs_bits(f[j]));
-        }
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const float scale = q8_scale(amax);
-        if (c0 < s.code_bytes) {
-            uint32_t word = 0;
-            for (int j = 0; j < 4; ++j) word |= q8_code(f[j], scale) << (8 * j);
-            *reinterpret_cast<uint32_t*>(row + c0) = word;
-        }
-        if (lane == 0) *reinterpret_cast<float*>(row + s.code_bytes + 4u * b) = scale;
+// z*r*w + b.
+template <typename T, bool kVec>
+__device__ __forceinline__ void scale_shift(const Cols<kVec>& c, float r, const void* w,
+                                            const void* b, F8& z) {
+    F8 wv;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], both(r));
+    if (w) {
+        load_vec<T, kVec>(w, 1.0f, c, wv);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], wv[k]);
     }
-    const uint64_t at = s.code_bytes + 4ull * s.blocks + 4ull * threadIdx.x;
-    if (at < s.row_bytes) *reinterpret_cast<uint32_t*>(row + at) = 0u;
+    if (b) {
+        load_vec<T, kVec>(b, 0.0f, c, wv);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = f2_add(z[k], wv[k]);
+    }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs p) {
-    extern __shared__ uint8_t smem[];
-    T* ys = reinterpret_cast<T*>(smem);   // y as stored, for its checkpoint
+// Checkpoint of a warp's chunks; many or 32-bit values one chunk after the other (registers).
+template <typename T, bool kVec, int G>
+__device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint32_t at,
+                                         uint32_t stride, uint32_t lane, const Raw<T> (&raw)[G]) {
+    if constexpr (sizeof(T) == 2 && G <= 2) {
+        save_chunks<T, kVec, G>(row, s, at, stride, lane, raw);
+    } else {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const Raw<T> one[1] = {raw[g]};
+            save_chunks<T, kVec, 1>(row, s, at + g * stride, stride, lane, one);
+        }
+    }
+}
+
+// Warps of a CTA at most. Four chunks of 32-bit values per lane need 255 registers; rows beyond
+// eight such warps are shared by the CTAs of a cluster.
+template <typename T, int G>
+constexpr int forward_warps() { return sizeof(T) * G == 16 ? 8 : kMaxWarps; }
+
+template <typename T, bool kVec, int G>
+__global__ void __launch_bounds__(32 * forward_warps<T, G>(), 1)
+    join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
+    __shared__ float part[2][kMaxWarps * kMaxCluster][4];
+    const uint32_t warp = threadIdx.x >> 5, team = warp / warps, teams = (blockDim.x >> 5) / warps;
+    uint32_t rank = 0;
+    if (ctas > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    Team t{part, threadIdx.x & 31u, warp - team * warps, team * warps, warps, ctas, rank, team + 1,
+           0};
+    const uint32_t first = rank * warps + t.warp, step = warps * ctas;   // this warp's chunks
+    const uint64_t cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
+    Cols<kVec> c[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) c[g] = Cols<kVec>(g * step + first, t.lane, p.cols);
     grid_wait();
-    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        auto h = [&](uint32_t c) { return read_at<T>(p.h, p.h_ckpt, p.ck, r, c); };
-        float hm, hr, ym, yr;
-        if (p.has_branch) row_stats(p.post, p.cols, p.post_eps, h, &hm, &hr);
-        auto y = [&](uint32_t c) {
-            float v = __fmul_rn(p.rs, read_at<T>(p.x, p.x_ckpt, p.ck, r, c));
-            if (p.has_branch) {
-                float z = h(c);
-                if (p.post != ZERO_NORM_NONE)
-                    z = __fmaf_rn(__fmul_rn(__fsub_rn(z, hm), hr), vec_at<T>(p.post_w, c, 1.0f),
-                                  vec_at<T>(p.post_b, c, 0.0f));
-                if (p.gate_rows)
-                    z = __fmul_rn(z, to_f(((const T*)p.gate.p)[(r / p.gate_rows) * p.gate.ld + c]));
-                v = __fmaf_rn(p.bs, z, v);
-            }
-            return v;
-        };
-        row_stats(p.u.p ? p.pre : ZERO_NORM_NONE, p.cols, p.pre_eps, y, &ym, &yr);
-        __syncthreads();
-        for (uint32_t c = threadIdx.x; c < p.cols; c += kThreads) {
-            const float v = y(c);
-            if (p.u.p)
-                ((T*)p.u.p)[r * p.u.ld + c] =
-                    from_f<T>(__fmaf_rn(__fmul_rn(__fsub_rn(v, ym), yr),
-                                        vec_at<T>(p.pre_w, c, 1.0f), vec_at<T>(p.pre_b, c, 0.0f)));
-            if (p.save_y) ys[c] = from_f<T>(v);
-            if (p.y.p) ((T*)p.y.p)[r * p.y.ld + c] = from_f<T>(v);
+    if (ctas > 1) team_barrier(t);   // every CTA is there before the first remote store
+    for (uint64_t r = cluster * teams + team; r < p.rows; r += clusters * teams) {
+        Raw<T> rx[G], rh[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            rx[g] = load_row<T, kVec>(p.x, p.x_ckpt, p.ck, r, c[g]);
+            if (p.has_branch) rh[g] = load_row<T, kVec>(p.h, p.h_ckpt, p.ck, r, c[g]);
         }
-        if (p.save_h) save_row<T>(p.save_h, p.ck, r, (const T*)p.h.p + r * p.h.ld);
-        if (p.save_y) {
-            __syncthreads();
-            save_row<T>(p.save_y, p.ck, r, ys);
-            __syncthreads();
+        if (p.save_h) {
+            uint8_t* row = p.save_h + r * p.ck.row_bytes;
+            save_all<T, kVec, G>(row, p.ck, first, step, t.lane, rh);
+            if (first == 0) save_pad(row, p.ck, t.lane);
         }
-    }
-}
-
-// The values of a boundary's gradient at one element, from its row's statistics.
-struct Grad {
-    float yh, hh, hn, gate, gy, t, gt, du;
-};
-
-template <typename T>
-__device__ __forceinline__ Grad grad_at(const JoinArgs& p, uint64_t r, uint32_t c, float hm,
-                                        float hr, float ym, float yr, float m1, float m2) {
-    Grad g = {};
-    if (p.du.p) {
-        g.du = to_f(((const T*)p.du.p)[r * p.du.ld + c]);
-        g.yh = __fmul_rn(__fsub_rn(read_at<T>(p.x, p.x_ckpt, p.ck, r, c), ym), yr);
-        const float gu = __fmul_rn(g.du, vec_at<T>(p.pre_w, c, 1.0f));
-        g.gy = __fmul_rn(yr, __fsub_rn(__fsub_rn(gu, m1), __fmul_rn(g.yh, m2)));
-    }
-    if (p.dy.p) g.gy = __fadd_rn(g.gy, to_f(((const T*)p.dy.p)[r * p.dy.ld + c]));
-    if (p.has_branch) {
-        g.gate = p.gate_rows ? to_f(((const T*)p.gate.p)[(r / p.gate_rows) * p.gate.ld + c]) : 1.0f;
-        g.t = __fmul_rn(__fmul_rn(p.bs, g.gate), g.gy);
-        g.gt = g.t;
-        if (p.h.p || p.h_ckpt) {
-            g.hn = read_at<T>(p.h, p.h_ckpt, p.ck, r, c);
+        F8 y[G];
+        if (p.has_branch) {
+            F8 h[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) widen_row<T>(rh[g], p.h_ckpt != nullptr, h[g]);
             if (p.post != ZERO_NORM_NONE) {
-                const float w = vec_at<T>(p.post_w, c, 1.0f);
-                g.hh = __fmul_rn(__fsub_rn(g.hn, hm), hr);
-                g.hn = __fmaf_rn(g.hh, w, vec_at<T>(p.post_b, c, 0.0f));
-                g.gt = __fmul_rn(g.t, w);
+                const float hr = centre<kVec, G>(t, p.post, p.post_eps, inv_cols, c, h);
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    scale_shift<T, kVec>(c[g], hr, p.post_w, p.post_b, h[g]);
+            }
+            if (p.gate_rows) {
+                const T* gate = (const T*)p.gate.p + row_over(r, p.gate_rows) * p.gate.ld;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    F8 gv;
+                    widen<T>(load_raw<T, kVec>(gate, c[g]), gv);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[g][k] = f2_mul(h[g][k], gv[k]);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                widen_row<T>(rx[g], p.x_ckpt != nullptr, y[g]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    y[g][k] = f2_fma(both(p.bs), h[g][k], f2_mul(both(p.rs), y[g][k]));
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                widen_row<T>(rx[g], p.x_ckpt != nullptr, y[g]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[g][k] = f2_mul(both(p.rs), y[g][k]);
+            }
+        }
+        if (p.y.p || p.save_y) {
+            Raw<T> ry[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                ry[g] = narrow<T>(y[g]);
+                if (p.y.p) store_raw<T, kVec>((T*)p.y.p + r * p.y.ld, c[g], ry[g]);
+            }
+            if (p.save_y) {
+                uint8_t* row = p.save_y + r * p.ck.row_bytes;
+#pragma unroll
+                for (int g = 0; g < G; ++g)   // a post bias may have filled missing columns
+                    if (c[g].mask != 0xffu) {
+                        F8 z;
+                        widen<T>(ry[g], z);
+                        clear_missing<kVec>(c[g], z);
+                        ry[g] = narrow<T>(z);
+                    }
+                save_all<T, kVec, G>(row, p.ck, first, step, t.lane, ry);
+                if (first == 0) save_pad(row, p.ck, t.lane);
+            }
+        }
+        if (p.u.p) {
+            const float yr = centre<kVec, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                scale_shift<T, kVec>(c[g], yr, p.pre_w, p.pre_b, y[g]);
+                store_raw<T, kVec>((T*)p.u.p + r * p.u.ld, c[g], narrow<T>(y[g]));
             }
         }
     }
-    return g;
+    if (ctas > 1) team_barrier(t);   // no CTA leaves while another may still store into it
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) join_back_kernel(JoinArgs p, float* stats) {
-    grid_wait();
-    for (uint64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        float hm = 0, hr = 1, ym = 0, yr = 1, m1 = 0, m2 = 0, n1 = 0, n2 = 0;
-        if (p.du.p) {
-            auto y = [&](uint32_t c) { return read_at<T>(p.x, p.x_ckpt, p.ck, r, c); };
-            row_stats(p.pre, p.cols, p.pre_eps, y, &ym, &yr);
-            float s1 = 0, s2 = 0;
-            for (uint32_t c = threadIdx.x; c < p.cols; c += kThreads) {
-                const float gu = __fmul_rn(to_f(((const T*)p.du.p)[r * p.du.ld + c]),
-                                           vec_at<T>(p.pre_w, c, 1.0f));
-                s1 = __fadd_rn(s1, gu);
-                s2 = __fmaf_rn(gu, __fmul_rn(__fsub_rn(y(c), ym), yr), s2);
-            }
-            m2 = __fdiv_rn(cta_sum(s2), (float)p.cols);
-            if (p.pre == ZERO_NORM_LAYER) m1 = __fdiv_rn(cta_sum(s1), (float)p.cols);
-        }
-        if (p.has_branch && p.post != ZERO_NORM_NONE) {
-            auto h = [&](uint32_t c) { return read_at<T>(p.h, p.h_ckpt, p.ck, r, c); };
-            row_stats(p.post, p.cols, p.post_eps, h, &hm, &hr);
-            float s1 = 0, s2 = 0;
-            for (uint32_t c = threadIdx.x; c < p.cols; c += kThreads) {
-                const Grad g = grad_at<T>(p, r, c, hm, hr, ym, yr, m1, m2);
-                s1 = __fadd_rn(s1, g.gt);
-                s2 = __fmaf_rn(g.gt, g.hh, s2);
-            }
-            n2 = __fdiv_rn(cta_sum(s2), (float)p.cols);
-            if (p.post == ZERO_NORM_LAYER) n1 = __fdiv_rn(cta_sum(s1), (float)p.cols);
-        }
-        if (stats && threadIdx.x == 0) {
-            float* s = stats + r * kRowStats;
-            s[0] = hm; s[1] = hr; s[2] = ym; s[3] = yr; s[4] = m1; s[5] = m2;
-        }
-        if (!p.dx.p && !p.dh.p) continue;
-        for (uint32_t c = threadIdx.x; c < p.cols; c += kThreads) {
-            const Grad g = grad_at<T>(p, r, c, hm, hr, ym, yr, m1, m2);
-            // dx may stand in dy's place: with vector gradients it is written by the second kernel
-            if (p.dx.p && (!stats || p.dx.p != p.dy.p))
-                ((T*)p.dx.p)[r * p.dx.ld + c] = from_f<T>(__fmul_rn(p.rs, g.gy));
-            if (p.dh.p)
-                ((T*)p.dh.p)[r * p.dh.ld + c] = from_f<T>(
-                    p.post == ZERO_NORM_NONE
-                        ? g.t
-                        : __fmul_rn(hr, __fsub_rn(__fsub_rn(g.gt, n1), __fmul_rn(g.hh, n2))));
-        }
-    }
+template <typename T, bool kVec, int G>
+cudaError_t run_forward(const JoinArgs& a, uint32_t warps, int sms, cudaStream_t stream) {
+    uint32_t ctas = 1;
+    while ((warps + ctas - 1) / ctas > (uint32_t)forward_warps<T, G>()) ctas *= 2;
+    warps = (warps + ctas - 1) / ctas;
+    const uint32_t teams = ctas == 1 && warps < 4 ? 4 / warps : 1;
+    const uint64_t clusters = (a.rows + teams - 1) / teams, cap = (uint64_t)sms * 32 / ctas;
+    return launch_clusters(join_kernel<T, kVec, G>,
+                           (unsigned)(clusters < cap ? clusters : cap), ctas, 32 * warps * teams,
+                           stream, a, warps, ctas, 1.0f / (float)a.cols);
 }
 
-template <typename T>
-__device__ __forceinline__ void put_sum(void* p, uint64_t at, float s, bool add) {
-    if (!p) return;
-    T* d = (T*)p + at;
-    *d = from_f<T>(add ? __fadd_rn(to_f(*d), s) : s);
-}
-
-// 32 columns, 8 rows at a time; the 8 partial sums are added in order.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) join_vectors_kernel(JoinArgs p, const float* stats) {
-    __shared__ float part[5][8][32];
-    grid_wait();
-    const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-    const uint32_t c = blockIdx.x * 32u + cx;
-    float s[5] = {};
-    auto flush = [&](int k, void* out, uint64_t at, bool add) {
-        part[k][ry][cx] = s[k];
-        __syncthreads();
-        if (ry == 0 && c < p.cols) {
-            float v = 0.0f;
-            for (int i = 0; i < 8; ++i) v = __fadd_rn(v, part[k][i][cx]);
-            put_sum<T>(out, at, v, add);
-        }
-        __syncthreads();
-        s[k] = 0.0f;
-    };
-    const uint64_t span = p.dgate.p ? p.gate_rows : p.rows;
-    for (uint64_t g0 = 0; g0 < p.rows; g0 += span) {
-        const uint64_t g1 = span < p.rows - g0 ? g0 + span : p.rows;
-        for (uint64_t r = g0 + ry; r < g1 && c < p.cols; r += 8) {
-            const float* st = stats + r * kRowStats;
-            const Grad g = grad_at<T>(p, r, c, st[0], st[1], st[2], st[3], st[4], st[5]);
-            s[0] = __fmaf_rn(__fmul_rn(p.bs, g.gy), g.hn, s[0]);
-            s[1] = __fmaf_rn(g.t, g.hh, s[1]);
-            s[2] = __fadd_rn(s[2], g.t);
-            s[3] = __fmaf_rn(g.du, g.yh, s[3]);
-            s[4] = __fadd_rn(s[4], g.du);
-            if (p.dx.p && p.dx.p == p.dy.p)
-                ((T*)p.dx.p)[r * p.dx.ld + c] = from_f<T>(__fmul_rn(p.rs, g.gy));
-        }
-        if (p.dgate.p) flush(0, p.dgate.p, g0 / span * p.dgate.ld + c, p.accumulate & ZERO_ACC_GATE);
-    }
-    const bool add = p.accumulate & ZERO_ACC_PARAMS;
-    flush(1, p.dpost_w, c, add);
-    flush(2, p.dpost_b, c, add);
-    flush(3, p.dpre_w, c, add);
-    flush(4, p.dpre_b, c, add);
+// Warps and chunks per lane of a row: as few warps as registers allow (one up to 1024 columns:
+// no exchange between warps), but one chunk per warp where there are too few rows to fill the
+// device anyway.
+template <typename T, bool kVec>
+cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
+    DevInfo di;
+    const cudaError_t e = dev_info(&di);
+    if (e != cudaSuccess) return e;
+    const uint32_t chunks = chunks_of(a.cols);
+    if (chunks <= kMaxWarps && a.rows <= (uint64_t)di.sms)
+        return run_forward<T, kVec, 1>(a, chunks, di.sms, stream);
+    if (chunks == 1) return run_forward<T, kVec, 1>(a, 1, di.sms, stream);
+    if (chunks == 2) return run_forward<T, kVec, 2>(a, 1, di.sms, stream);
+    if (chunks <= 4) return run_forward<T, kVec, 4>(a, 1, di.sms, stream);
+    if (chunks <= 16) return run_forward<T, kVec, 2>(a, (chunks + 1) / 2, di.sms, stream);
+    return run_forward<T, kVec, 4>(a, (chunks + 3) / 4, di.sms, stream);
 }
 
 template <typename T>
 cudaError_t run_join(const JoinArgs& a, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(a.rows < (1u << 20) ? a.rows : (1u << 20));
-    return launch_act(join_kernel<T>, dim3(grid), kThreads, a.save_y ? a.cols * sizeof(T) : 0,
-                      stream, a);
-}
-
-template <typename T>
-cudaError_t run_join_back(const JoinArgs& a, void* ws, cudaStream_t stream) {
-    const bool vec = a.dgate.p || a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b;
-    if (a.rows) {
-        const unsigned grid = (unsigned)(a.rows < (1u << 20) ? a.rows : (1u << 20));
-        const cudaError_t e = launch_act(join_back_kernel<T>, dim3(grid), kThreads, 0, stream, a,
-                                         vec ? (float*)ws : (float*)nullptr);
-        if (e != cudaSuccess) return e;
-    }
-    if (!vec) return cudaSuccess;
-    return launch_act(join_vectors_kernel<T>, dim3((a.cols + 31) / 32), kThreads, 0, stream, a,
-                      (const float*)ws);
+    return all_aligned<T>(a) ? run_forward_any<T, true>(a, stream)
+                             : run_forward_any<T, false>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream) {
-    if (dtype == ZERO_F32 && a.save_y) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            join_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            ZERO_JOIN_MAX_COLS * (int)sizeof(float));
-        if (e != cudaSuccess) return e;
-    }
     return dtype == ZERO_F16    ? run_join<__half>(a, stream)
            : dtype == ZERO_BF16 ? run_join<bf16>(a, stream)
                                 : run_join<float>(a, stream);
-}
-
-cudaError_t launch_join_backward(const JoinArgs& a, int dtype, void* ws, cudaStream_t stream) {
-    return dtype == ZERO_F16    ? run_join_back<__half>(a, ws, stream)
-           : dtype == ZERO_BF16 ? run_join_back<bf16>(a, ws, stream)
-                                : run_join_back<float>(a, ws, stream);
 }
 
 }  // namespace zk

@@ -1,0 +1,418 @@
+// Gradient of the block boundary for sm_100a (see zero_join.cu for the forward pass).
+//
+// Bound by HBM: dy, du and the saved y and h (bytes, where they are checkpoints) are read once,
+// dx and dh written once. Persistent teams of warps walk their rows with the next row's loads in
+// flight and keep the column sums (of the weights', biases' and gate's gradients) in registers;
+// the teams of a CTA are added through shared memory, the CTAs by a second kernel, always in the
+// same order. Rows wider than a CTA's warps are shared by the CTAs of a cluster, whose sums meet
+// in distributed shared memory.
+//
+// The statistics are computed again from the saved rows. The sums of g and g*(z - mean) that a
+// norm's gradient needs ride along with its second statistic, so a LayerNorm before the next
+// block costs two exchanges per row (RMS: one) and a norm after the block one more.
+#include "zero_join.cuh"
+
+namespace zk {
+namespace {
+
+constexpr int kMaxParts = 148;         // clusters that leave partial column sums
+
+// ---------------------------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------------------------
+// How a call's rows and columns are dealt out. A unit is a run of rows within one gate row (all
+// rows where no gate gradient is asked for): `parts` units of part_rows rows per gate row.
+struct BackGeom {
+    uint32_t warps, ctas, teams;   // warps of a CTA per row, CTAs per row, rows a CTA has in hand
+    uint32_t clusters;
+    uint64_t group_rows, parts, part_rows, units;
+    float inv_cols;
+};
+
+BackGeom back_geom(uint64_t rows, uint64_t cols, uint64_t group_rows, uint32_t most_warps,
+                   uint32_t sms) {
+    BackGeom g = {};
+    const uint32_t chunks = chunks_of(cols);
+    g.ctas = 1;
+    while ((chunks + g.ctas - 1) / g.ctas > most_warps) g.ctas *= 2;
+    g.warps = (chunks + g.ctas - 1) / g.ctas;
+    g.teams = g.ctas > 1 ? 1 : most_warps / g.warps;
+    uint64_t clusters = sms / g.ctas;
+    if (clusters > kMaxParts) clusters = kMaxParts;
+    const uint64_t useful = (rows + g.teams - 1) / g.teams;
+    if (clusters > useful) clusters = useful;
+    if (clusters < 1) clusters = 1;
+    g.clusters = (uint32_t)clusters;
+    g.group_rows = group_rows && group_rows < rows ? group_rows : rows;
+    if (g.group_rows) {
+        const uint64_t groups = (rows + g.group_rows - 1) / g.group_rows;
+        uint64_t parts = (uint64_t)g.clusters * g.teams / groups;
+        if (parts < 1) parts = 1;
+        g.part_rows = (g.group_rows + parts - 1) / parts;
+        g.parts = (g.group_rows + g.part_rows - 1) / g.part_rows;
+        g.units = groups * g.parts;
+    }
+    g.inv_cols = 1.0f / (float)cols;
+    return g;
+}
+
+// A team's place in its rows.
+struct Walk {
+    uint64_t unit, row, end;
+    __device__ __forceinline__ void open(const BackGeom& g, uint64_t rows) {
+        while (unit < g.units) {
+            const uint64_t group = row_over(unit, g.parts), part = unit - group * g.parts;
+            const uint64_t first = group * g.group_rows;
+            uint64_t last = first + g.group_rows < rows ? first + g.group_rows : rows;
+            row = first + part * g.part_rows;
+            end = row + g.part_rows < last ? row + g.part_rows : last;
+            if (row < end) return;
+            unit += (uint64_t)g.clusters * g.teams;
+        }
+    }
+    // to the next row; true if it belongs to another unit
+    __device__ __forceinline__ bool next(const BackGeom& g, uint64_t rows) {
+        if (++row < end) return false;
+        unit += (uint64_t)g.clusters * g.teams;
+        open(g, rows);
+        return true;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void put_sum(void* p, uint64_t at, float s, bool add) {
+    T* d = (T*)p + at;
+    *d = from_f<T>(add ? __fadd_rn(to_f(*d), s) : s);
+}
+
+// The partial sums of the vector gradients in the workspace: [cluster][4][cols], then the parts
+// of the gate's gradient: [unit][cols].
+__host__ __device__ __forceinline__ uint64_t vector_partials(uint32_t cols) {
+    return (uint64_t)kMaxParts * 4 * cols;
+}
+
+template <typename T>
+constexpr int back_warps() { return sizeof(T) == 4 ? 8 : 16; }   // registers: 255 and 128
+
+template <typename T, bool kVec, bool kPost, bool kGate>
+__global__ void __launch_bounds__(32 * back_warps<T>())
+    join_back_kernel(const __grid_constant__ JoinArgs p, const __grid_constant__ BackGeom g,
+                     float* ws) {
+    __shared__ float part[2][kMaxWarps * kMaxCluster][4];
+    // the gate's column sums, and with a norm after the block that norm's bias sums too: beside
+    // them the registers do not suffice. At the end the teams' sums meet here.
+    constexpr bool kSharedBias = kPost && kGate;
+    __shared__ float held[kSharedBias ? 2 : 1][back_warps<T>()][8][32];
+    const uint32_t warp = threadIdx.x >> 5, team = warp / g.warps;
+    uint32_t rank = 0;
+    if (g.ctas > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const uint32_t cluster = g.ctas > 1 ? blockIdx.x / g.ctas : blockIdx.x;
+    Team t{part, threadIdx.x & 31u, warp - team * g.warps, team * g.warps, g.warps, g.ctas, rank,
+           team + 1, 0};
+    const Cols<kVec> c(rank * g.warps + t.warp, t.lane, p.cols);
+    const bool has_du = p.du.p != nullptr;
+    const bool y_codes = p.x_ckpt != nullptr, h_codes = p.h_ckpt != nullptr;
+    const bool pre_layer = has_du && p.pre == ZERO_NORM_LAYER;
+    const bool post_layer = kPost && p.post == ZERO_NORM_LAYER;
+    F8 sum_pw = {}, sum_pb = {}, sum_qw = {}, sum_qb = {};
+    if (kGate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            held[0][warp][j][t.lane] = held[kSharedBias][warp][j][t.lane] = 0.0f;
+    }
+    grid_wait();
+    if (g.ctas > 1) team_barrier(t);   // every CTA of the cluster is there before the first store
+
+    Walk at{(uint64_t)cluster * g.teams + team, 0, 0};
+    at.open(g, p.rows);
+    Raw<T> ry, rh, rdu;
+    auto fetch = [&](uint64_t r) {
+        if (has_du) {
+            ry = load_row<T, kVec>(p.x, p.x_ckpt, p.ck, r, c);
+            rdu = load_raw<T, kVec>((const T*)p.du.p + r * p.du.ld, c);
+        }
+        if (kPost || kGate) rh = load_row<T, kVec>(p.h, p.h_ckpt, p.ck, r, c);
+    };
+    if (at.unit < g.units) fetch(at.row);
+    while (at.unit < g.units) {
+        const uint64_t r = at.row, unit = at.unit;
+        Raw<T> rdy;   // not needed before the first exchange: no load ahead
+        if (p.dy.p) rdy = load_raw<T, kVec>((const T*)p.dy.p + r * p.dy.ld, c);
+        F8 y, h, du, gu, gy;
+        if (has_du) {
+            widen_row<T>(ry, y_codes, y);
+            widen<T>(rdu, du);
+        }
+        if (kPost || kGate) widen_row<T>(rh, h_codes, h);
+        const bool turn = at.next(g, p.rows);
+        if (at.unit < g.units) fetch(at.row);   // the next row, while this one is worked on
+
+        if (pre_layer || post_layer) {
+            float s[2] = {pre_layer ? sum8(y) : 0.0f, post_layer ? sum8(h) : 0.0f};
+            team_sum<2>(t, s);
+            if (pre_layer) {
+                const uint64_t m = both(__fmul_rn(s[0], -g.inv_cols));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = f2_add(y[k], m);
+                clear_missing<kVec>(c, y);
+            }
+            if (post_layer) {
+                const uint64_t m = both(__fmul_rn(s[1], -g.inv_cols));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = f2_add(h[k], m);
+                clear_missing<kVec>(c, h);
+            }
+        }
+        float hr = 1.0f, yr = 0.0f, m1 = 0.0f, m2 = 0.0f;
+        if (has_du || kPost) {
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (has_du) {
+                F8 w;
+                load_vec<T, kVec>(p.pre_w, 1.0f, c, w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) gu[k] = f2_mul(du[k], w[k]);
+                s[0] = dot8(y, y);
+                s[1] = sum8(gu);
+                s[2] = dot8(gu, y);
+            }
+            if (kPost) s[3] = dot8(h, h);
+            team_sum<4>(t, s);
+            if (kPost)
+                hr = __frsqrt_rn(__fadd_rn(__fmul_rn(s[3], g.inv_cols), p.post_eps));
+            if (has_du) {
+                yr = __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], g.inv_cols), p.pre_eps));
+                m1 = pre_layer ? __fmul_rn(s[1], g.inv_cols) : 0.0f;
+                m2 = __fmul_rn(__fmul_rn(s[2], yr), g.inv_cols);
+            }
+        }
+        if (p.dy.p) {
+            widen<T>(rdy, gy);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) gy[k] = 0;
+        }
+        if (has_du) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t yh = f2_mul(y[k], both(yr));
+                sum_pw[k] = f2_fma(du[k], yh, sum_pw[k]);
+                sum_pb[k] = f2_add(sum_pb[k], du[k]);
+                const uint64_t d = f2_fma(yh, both(-m2), f2_add(gu[k], both(-m1)));
+                gy[k] = f2_fma(both(yr), d, gy[k]);
+            }
+            if (pre_layer) clear_missing<kVec>(c, gy);
+        }
+        if (p.dx.p) {
+            F8 dx;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dx[k] = f2_mul(both(p.rs), gy[k]);
+            store_raw<T, kVec>((T*)p.dx.p + r * p.dx.ld, c, narrow<T>(dx));
+        }
+        if (p.has_branch && (kPost || kGate || p.dh.p)) {
+            F8 b;   // t = bs*gate*gy
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[k] = f2_mul(both(p.bs), gy[k]);
+            F8 v;
+            if (kPost) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = f2_mul(h[k], both(hr));
+            }
+            if (kGate) {
+                F8 w;
+                load_vec<T, kVec>(kPost ? p.post_w : nullptr, 1.0f, c, w);
+                load_vec<T, kVec>(kPost ? p.post_b : nullptr, 0.0f, c, v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float* sum = &held[0][warp][2 * k][t.lane];
+                    f2_unpack(f2_fma(b[k], kPost ? f2_fma(h[k], w[k], v[k]) : h[k],
+                                     f2_pack(sum[0], sum[32])),
+                              sum[0], sum[32]);
+                }
+            }
+            if (p.gate_rows) {
+                widen<T>(load_raw<T, kVec>((const T*)p.gate.p +
+                                               row_over(r, p.gate_rows) * p.gate.ld, c), v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) b[k] = f2_mul(b[k], v[k]);
+            }
+            if (kPost) {
+                load_vec<T, kVec>(p.post_w, 1.0f, c, v);
+                float s[2];
+                F8 gt;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    sum_qw[k] = f2_fma(b[k], h[k], sum_qw[k]);
+                    if (kSharedBias) {
+                        float* sum = &held[kSharedBias][warp][2 * k][t.lane];
+                        f2_unpack(f2_add(b[k], f2_pack(sum[0], sum[32])), sum[0], sum[32]);
+                    } else {
+                        sum_qb[k] = f2_add(sum_qb[k], b[k]);
+                    }
+                    gt[k] = f2_mul(b[k], v[k]);
+                }
+                if (p.dh.p) {
+                    s[0] = sum8(gt);
+                    s[1] = dot8(gt, h);
+                    team_sum<2>(t, s);
+                    const float n1 = post_layer ? __fmul_rn(s[0], g.inv_cols) : 0.0f;
+                    const float n2 = __fmul_rn(s[1], g.inv_cols);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        gt[k] = f2_mul(both(hr),
+                                       f2_fma(h[k], both(-n2), f2_add(gt[k], both(-n1))));
+                    store_raw<T, kVec>((T*)p.dh.p + r * p.dh.ld, c, narrow<T>(gt));
+                }
+            } else if (p.dh.p) {
+                store_raw<T, kVec>((T*)p.dh.p + r * p.dh.ld, c, narrow<T>(b));
+            }
+        }
+        if (kGate && turn) {   // the unit's part of its gate row's gradient
+            const uint64_t group = row_over(unit, g.parts);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float f = held[0][warp][j][t.lane];
+                held[0][warp][j][t.lane] = 0.0f;
+                if (!(c.mask >> j & 1u)) continue;
+                if (g.parts > 1)
+                    ws[vector_partials(p.cols) + unit * p.cols + c.at(j)] = f;
+                else
+                    put_sum<T>(p.dgate.p, group * p.dgate.ld + c.at(j), f,
+                               p.accumulate & ZERO_ACC_GATE);
+            }
+        }
+    }
+    if (ws) grid_launch_next();
+    // the teams' column sums, added in order; to the workspace, or as they are if one CTA had all
+    void* const outs[4] = {p.dpost_w, p.dpost_b, p.dpre_w, p.dpre_b};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (!outs[k]) continue;
+        const bool there = kSharedBias && k == 1;
+        float(*comb)[8][32] = held[there];
+        __syncthreads();
+        if (!there) {
+            const F8& s = k == 0 ? sum_qw : k == 1 ? sum_qb : k == 2 ? sum_pw : sum_pb;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f2_unpack(s[j], comb[warp][2 * j][t.lane], comb[warp][2 * j + 1][t.lane]);
+            __syncthreads();
+        }
+        if (team != 0) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!(c.mask >> j & 1u)) continue;
+            float v = 0.0f;
+            for (uint32_t i = 0; i < g.teams; ++i)
+                v = __fadd_rn(v, comb[i * g.warps + t.warp][j][t.lane]);
+            if (g.clusters > 1)
+                ws[((uint64_t)cluster * 4 + k) * p.cols + c.at(j)] = v;
+            else
+                put_sum<T>(outs[k], c.at(j), v, p.accumulate & ZERO_ACC_PARAMS);
+        }
+    }
+    if (g.ctas > 1) team_barrier(t);   // no CTA leaves while another may still store into it
+}
+
+// Column sums from the workspace: 32 columns by 16 rows of partial sums per CTA. blockIdx.y < 4:
+// a vector's (if they are split); above, a gate row's. Without partial sums (no rows): zeros.
+constexpr int kSumRows = 16;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kSumRows)
+    join_vectors_kernel(const __grid_constant__ JoinArgs p, const __grid_constant__ BackGeom g,
+                        bool vectors, const float* ws) {
+    __shared__ float part[kSumRows][32];
+    grid_wait();
+    const uint32_t cx = threadIdx.x & 31u, ry = threadIdx.x >> 5, c = blockIdx.x * 32u + cx;
+    const uint32_t k = blockIdx.y;
+    void* out = k == 0 ? p.dpost_w : k == 1 ? p.dpost_b : k == 2 ? p.dpre_w : k == 3 ? p.dpre_b
+                                                                          : p.dgate.p;
+    if (!out || (k < 4 && !vectors)) return;
+    const uint64_t stride = k < 4 ? 4ull * p.cols : p.cols;
+    const float* src = k < 4 ? ws + (uint64_t)k * p.cols
+                             : ws + vector_partials(p.cols) + (k - 4) * g.parts * p.cols;
+    uint64_t n = p.rows ? g.clusters : 0;
+    if (k >= 4) {   // the last gate row may be shorter: parts that have rows
+        const uint64_t left = p.rows - (k - 4) * g.group_rows;
+        n = ((left < g.group_rows ? left : g.group_rows) + g.part_rows - 1) / g.part_rows;
+    }
+    float s = 0.0f;
+    if (c < p.cols) {
+#pragma unroll 4
+        for (uint64_t i = ry; i < n; i += kSumRows) s = __fadd_rn(s, src[i * stride + c]);
+    }
+    part[ry][cx] = s;
+    __syncthreads();
+    if (ry != 0 || c >= p.cols) return;
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSumRows; ++i) v = __fadd_rn(v, part[i][cx]);
+    if (k < 4)
+        put_sum<T>(out, c, v, p.accumulate & ZERO_ACC_PARAMS);
+    else
+        put_sum<T>(out, (uint64_t)(k - 4) * p.dgate.ld + c, v, p.accumulate & ZERO_ACC_GATE);
+}
+
+template <typename T, bool kVec, bool kPost, bool kGate>
+cudaError_t run_back_kernel(const JoinArgs& a, const BackGeom& g, float* ws,
+                            cudaStream_t stream) {
+    return launch_clusters(join_back_kernel<T, kVec, kPost, kGate>, g.clusters, g.ctas,
+                           32 * g.warps * g.teams, stream, a, g, ws);
+}
+
+template <typename T, bool kVec>
+cudaError_t run_back_any(const JoinArgs& a, const BackGeom& g, float* ws, cudaStream_t stream) {
+    const bool post = a.post != ZERO_NORM_NONE && (a.dh.p || a.dgate.p || a.dpost_w || a.dpost_b);
+    if (post)
+        return a.dgate.p ? run_back_kernel<T, kVec, true, true>(a, g, ws, stream)
+                         : run_back_kernel<T, kVec, true, false>(a, g, ws, stream);
+    return a.dgate.p ? run_back_kernel<T, kVec, false, true>(a, g, ws, stream)
+                     : run_back_kernel<T, kVec, false, false>(a, g, ws, stream);
+}
+
+template <typename T>
+cudaError_t run_join_back(const JoinArgs& a, float* ws, cudaStream_t stream) {
+    DevInfo di;
+    cudaError_t e = dev_info(&di);
+    if (e != cudaSuccess) return e;
+    const bool vec = a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b;
+    const BackGeom g = back_geom(a.rows, a.cols, a.dgate.p ? a.gate_rows : 0,
+                                 (uint32_t)back_warps<T>(), (uint32_t)di.sms);
+    const bool vectors = vec && (g.clusters > 1 || a.rows == 0);
+    const bool split = vectors || (a.dgate.p && g.parts > 1);
+    if (a.rows) {
+        e = all_aligned<T>(a) ? run_back_any<T, true>(a, g, split ? ws : nullptr, stream)
+                              : run_back_any<T, false>(a, g, split ? ws : nullptr, stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (!split) return cudaSuccess;
+    const uint64_t gates = a.dgate.p && g.parts > 1 ? g.units / g.parts : 0;
+    return launch_act(join_vectors_kernel<T>, dim3((a.cols + 31) / 32, (unsigned)(4 + gates)),
+                      32 * kSumRows, 0, stream, a, g, vectors, (const float*)ws);
+}
+
+}  // namespace
+
+// Enough for every type and set of outputs: the vectors' partial sums, and a partial gate row
+// per team where a gate row's rows may be dealt to several.
+uint64_t join_workspace(uint64_t rows, uint64_t cols, uint64_t gate_rows) {
+    if (cols == 0) return 0;
+    uint64_t floats = vector_partials((uint32_t)cols);
+    if (gate_rows && rows) {
+        uint64_t most = 0;
+        for (const uint32_t warps : {8u, 16u}) {
+            const BackGeom g = back_geom(rows, cols, gate_rows, warps, kMaxParts);
+            if (g.parts > 1 && g.units > most) most = g.units;
+        }
+        floats += most * cols;
+    }
+    return (floats * 4 + 15) / 16 * 16;
+}
+
+cudaError_t launch_join_backward(const JoinArgs& a, int dtype, void* ws, cudaStream_t stream) {
+    return dtype == ZERO_F16    ? run_join_back<__half>(a, (float*)ws, stream)
+           : dtype == ZERO_BF16 ? run_join_back<bf16>(a, (float*)ws, stream)
+                                : run_join_back<float>(a, (float*)ws, stream);
+}
+
+}  // namespace zk
