@@ -810,8 +810,9 @@ zero_status zero_ckpt_wgrad_q8(uint64_t tokens, uint64_t out_features, uint64_t 
  * Matrices: dtype, element-aligned, row strides ld* in elements (>= cols); vectors (post_w ...)
  * contiguous; checkpoints 16-byte aligned. y may be x itself (same address and stride); no other
  * output may overlap an input or another output.
- * Errors: ZERO_EINVAL (the rules above, cols > ZERO_JOIN_MAX_COLS, unknown dtype or norm, eps
- * negative or not finite, scales not finite, overlap), ZERO_EALIGN, ZERO_ECUDA. rows or
+ * Errors: ZERO_EINVAL (the rules above, cols > ZERO_JOIN_MAX_COLS, rows or a row's stride in
+ * bytes at or above 2^31, unknown dtype or norm, eps negative or not finite, scales not finite,
+ * overlap), ZERO_EALIGN, ZERO_ECUDA. rows or
  * cols == 0 launches nothing.
  * ---------------------------------------------------------------------------------------- */
 #define ZERO_JOIN_MAX_COLS 16384

@@ -139,23 +139,31 @@ __device__ __forceinline__ const float* ckpt_scales(const uint8_t* row, const Ck
 
 // ---------------------------------------------------------------------------------------------
 // Eight columns per lane. A warp covers 256 columns (two blocks of codes) of a row. With 16-byte
-// aligned rows (kVec) a lane's columns are neighbours and move as 16-byte accesses; otherwise
-// lane l takes columns l, l + 32, ..., so that a warp's narrow accesses still touch whole sectors.
+// aligned rows a lane's columns are neighbours and move as 16-byte accesses (kWide: a row ends on
+// a lane's last column; kTail: it may end inside a lane's columns). Otherwise (kNarrow) lane l
+// takes columns l, l + 32, ..., so that a warp's narrow accesses still touch whole sectors.
 // ---------------------------------------------------------------------------------------------
 constexpr uint32_t kWarpCols = 256;
 
-template <bool kVec>
+enum Access { kNarrow = 0, kTail = 1, kWide = 2 };
+
+template <int kA>
 struct Cols {
     uint32_t c0, cols;
     uint32_t mask;   // bit j: column j exists
     __device__ __forceinline__ Cols() : c0(0), cols(0), mask(0) {}
     __device__ __forceinline__ Cols(uint32_t chunk, uint32_t lane, uint32_t n) : cols(n), mask(0) {
-        c0 = chunk * kWarpCols + (kVec ? 8u * lane : lane);
+        c0 = chunk * kWarpCols + (kA == kNarrow ? lane : 8u * lane);
         const uint32_t left = n > c0 ? n - c0 : 0u;
-        const uint32_t count = kVec ? left : (left + 31u) / 32u;
+        const uint32_t count = kA == kNarrow ? (left + 31u) / 32u : left;
         mask = count >= 8u ? 0xffu : (1u << count) - 1u;
     }
-    __device__ __forceinline__ uint32_t at(int j) const { return c0 + (kVec ? j : 32 * j); }
+    __device__ __forceinline__ uint32_t at(int j) const {
+        return c0 + (kA == kNarrow ? 32 * j : j);
+    }
+    __device__ __forceinline__ bool any() const { return mask != 0; }
+    // every column of the lane exists (kWide: or none does)
+    __device__ __forceinline__ bool whole() const { return kA == kWide ? any() : mask == 0xffu; }
 };
 
 // Eight values as they lie in memory: T, or codes (two words) and the scales of the lane's first
@@ -165,10 +173,12 @@ struct Raw {
     uint32_t w[2 * sizeof(T)];
 };
 
-template <typename T, bool kVec>
-__device__ __forceinline__ Raw<T> load_raw(const T* row, const Cols<kVec>& c) {
+template <typename T, int kA>
+__device__ __forceinline__ Raw<T> load_raw(const T* row, const Cols<kA>& c) {
     Raw<T> r;
-    if (kVec && c.mask == 0xffu) {
+#pragma unroll
+    for (int k = 0; k < 2 * (int)sizeof(T); ++k) r.w[k] = 0;
+    if (kA != kNarrow && c.whole()) {
         const uint4* p = reinterpret_cast<const uint4*>(row + c.c0);
 #pragma unroll
         for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
@@ -180,42 +190,52 @@ __device__ __forceinline__ Raw<T> load_raw(const T* row, const Cols<kVec>& c) {
         }
         return r;
     }
-#pragma unroll
-    for (int k = 0; k < 2 * (int)sizeof(T); ++k) r.w[k] = 0;
+    if (kA == kWide || !c.any()) return r;
+    // every load is issued (a missing column reads the lane's first one), then sorted out: the
+    // loads do not wait for one another
+    uint32_t v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        if (!(c.mask >> j & 1u)) continue;
-        if constexpr (sizeof(T) == 4) {
-            r.w[j] = reinterpret_cast<const uint32_t*>(row)[c.at(j)];
-        } else {
-            r.w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c.at(j)] << 16 * (j & 1);
-        }
+        const uint32_t i = c.mask >> j & 1u ? c.at(j) : c.c0;
+        if constexpr (sizeof(T) == 4)
+            v[j] = reinterpret_cast<const uint32_t*>(row)[i];
+        else
+            v[j] = reinterpret_cast<const uint16_t*>(row)[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t x = c.mask >> j & 1u ? v[j] : 0u;
+        if constexpr (sizeof(T) == 4)
+            r.w[j] = x;
+        else
+            r.w[j / 2] |= x << 16 * (j & 1);
     }
     return r;
 }
 
-template <typename T, bool kVec>
+template <typename T, int kA>
 __device__ __forceinline__ Raw<T> load_codes(const uint8_t* row, const CkptShape& s,
-                                             const Cols<kVec>& c) {
+                                             const Cols<kA>& c) {
     Raw<T> r;
     r.w[0] = r.w[1] = 0x80808080u;
     r.w[2] = r.w[3] = 0u;
-    if (c.mask == 0) return r;
+    if (!c.any()) return r;
     const float* sc = ckpt_scales(row, s);
-    if constexpr (kVec) {
+    if constexpr (kA != kNarrow) {
         const uint2 q = *reinterpret_cast<const uint2*>(row + c.c0);
         r.w[0] = q.x;
         r.w[1] = q.y;
         r.w[2] = r.w[3] = __float_as_uint(sc[c.c0 >> 7]);
     } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = row[c.mask >> j & 1u ? c.at(j) : c.c0];
+        r.w[2] = __float_as_uint(sc[c.c0 >> 7]);
+        r.w[3] = __float_as_uint(sc[(c.c0 >> 7) + (c.mask >> 4 & 1u)]);
+        r.w[0] = r.w[1] = 0u;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (c.mask >> j & 1u) {
-                const uint32_t sh = 8 * (j & 3);
-                r.w[j / 4] = (r.w[j / 4] & ~(255u << sh)) | (uint32_t)row[c.at(j)] << sh;
-            }
-        r.w[2] = __float_as_uint(sc[c.c0 >> 7]);
-        if (c.mask & 0xf0u) r.w[3] = __float_as_uint(sc[(c.c0 >> 7) + 1]);
+            r.w[j / 4] |= (c.mask >> j & 1u ? v[j] : 128u) << 8 * (j & 3);
     }
     return r;
 }
@@ -252,12 +272,18 @@ __device__ __forceinline__ void widen_codes(const Raw<T>& r, F8& v) {
     }
 }
 
-// The row r of a matrix or of a checkpoint, and its values.
-template <typename T, bool kVec>
-__device__ __forceinline__ Raw<T> load_row(const Mat& m, const uint8_t* ck, const CkptShape& s,
-                                           uint64_t r, const Cols<kVec>& c) {
-    if (ck) return load_codes<T, kVec>(ck + r * s.row_bytes, s, c);
-    return load_raw<T, kVec>((const T*)m.p + r * m.ld, c);
+// Row r of a matrix whose rows lie `pitch` bytes apart (both below 2^32: one multiply-add).
+template <typename T>
+__device__ __forceinline__ T* row_of(const Rows& m, uint32_t r) {
+    return reinterpret_cast<T*>(reinterpret_cast<char*>(m.p) + (uint64_t)r * m.pitch);
+}
+
+// The values of a row of a matrix or of a checkpoint.
+template <typename T, int kA>
+__device__ __forceinline__ Raw<T> load_row(const Rows& m, bool codes, const CkptShape& s,
+                                           uint32_t r, const Cols<kA>& c) {
+    if (codes) return load_codes<T, kA>(row_of<uint8_t>(m, r), s, c);
+    return load_raw<T, kA>(row_of<T>(m, r), c);
 }
 
 template <typename T>
@@ -269,10 +295,10 @@ __device__ __forceinline__ void widen_row(const Raw<T>& raw, bool codes, F8& v) 
 }
 
 // A vector of cols values, or `none` everywhere.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_vec(const void* p, float none, const Cols<kVec>& c, F8& v) {
+template <typename T, int kA>
+__device__ __forceinline__ void load_vec(const void* p, float none, const Cols<kA>& c, F8& v) {
     if (p) {
-        widen<T>(load_raw<T, kVec>((const T*)p, c), v);
+        widen<T>(load_raw<T, kA>((const T*)p, c), v);
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = f2_pack(none, none);
@@ -280,8 +306,13 @@ __device__ __forceinline__ void load_vec(const void* p, float none, const Cols<k
 }
 
 // Zero the columns that do not exist.
-template <bool kVec>
-__device__ __forceinline__ void clear_missing(const Cols<kVec>& c, F8& v) {
+template <int kA>
+__device__ __forceinline__ void clear_missing(const Cols<kA>& c, F8& v) {
+    if (kA == kWide) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = c.any() ? v[k] : 0;
+        return;
+    }
     if (c.mask == 0xffu) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -325,15 +356,16 @@ __device__ __forceinline__ Raw<T> narrow(const F8& v) {
     return r;
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void store_raw(T* row, const Cols<kVec>& c, const Raw<T>& r) {
-    if (kVec && c.mask == 0xffu) {
+template <typename T, int kA>
+__device__ __forceinline__ void store_raw(T* row, const Cols<kA>& c, const Raw<T>& r) {
+    if (kA != kNarrow && c.whole()) {
         uint4* p = reinterpret_cast<uint4*>(row + c.c0);
 #pragma unroll
         for (int k = 0; k < (int)sizeof(T) / 2; ++k)
             p[k] = make_uint4(r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]);
         return;
     }
+    if (kA == kWide) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         if (!(c.mask >> j & 1u)) continue;
@@ -360,18 +392,18 @@ __device__ __forceinline__ uint32_t amax1(uint32_t h) {
     return max(h & 0x7fffu, h >> 16 & 0x7fffu);
 }
 
-// Largest magnitude of the lane's first and second four columns, or (kVec) of all in m[0].
-template <typename T, bool kVec>
+// Largest magnitude of the lane's first and second four columns, or (neighbours) of all in m[0].
+template <typename T, int kA>
 __device__ __forceinline__ void lane_amax(const Raw<T>& r, uint32_t (&m)[2]) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             m[k] = max(max(r.w[4 * k] & 0x7fffffffu, r.w[4 * k + 1] & 0x7fffffffu),
                        max(r.w[4 * k + 2] & 0x7fffffffu, r.w[4 * k + 3] & 0x7fffffffu));
-        if (kVec) m[0] = max(m[0], m[1]);
+        if (kA != kNarrow) m[0] = max(m[0], m[1]);
     } else {
         const uint32_t a = amax2<T>(r.w[0], r.w[1]), b = amax2<T>(r.w[2], r.w[3]);
-        if constexpr (kVec) {
+        if constexpr (kA != kNarrow) {
             m[0] = amax1(amax2<T>(a, b));
         } else {
             m[0] = amax1(a);
@@ -389,11 +421,11 @@ __device__ __forceinline__ uint32_t amax_bits(uint32_t m) {
 }
 
 // The largest magnitude of each of the warp's two blocks, the same in every lane.
-template <typename T, bool kVec>
+template <typename T, int kA>
 __device__ __forceinline__ void block_amax(const Raw<T>& r, uint32_t lane, uint32_t (&a)[2]) {
     uint32_t m[2];
-    lane_amax<T, kVec>(r, m);
-    if constexpr (kVec) {   // 16 lanes per block
+    lane_amax<T, kA>(r, m);
+    if constexpr (kA != kNarrow) {   // 16 lanes per block
         m[1] = lane < 16u ? 0u : m[0];
         m[0] = lane < 16u ? m[0] : 0u;
     }
@@ -403,8 +435,8 @@ __device__ __forceinline__ void block_amax(const Raw<T>& r, uint32_t lane, uint3
 
 // The code words of N chunks of a warp; every value first takes the short way, so that
 // the chunks' instructions interleave and one branch covers them all. scale, inv: of the lane's
-// block (kVec), or of the blocks of its first and second four columns.
-template <typename T, bool kVec, int N>
+// block (neighbours), or of the blocks of its first and second four columns.
+template <typename T, int kA, int N>
 __device__ __forceinline__ void make_codes(const Raw<T> (&raw)[N], const float (&scale)[N][2],
                                            const float (&inv)[N][2], uint2 (&w)[N]) {
     bool fine[N];
@@ -416,7 +448,7 @@ __device__ __forceinline__ void make_codes(const Raw<T> (&raw)[N], const float (
         widen<T>(raw[k], v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f2_unpack(v[j], x[2 * j], x[2 * j + 1]);
-        fine[k] = q8_codes(x, scale[k][0], scale[k][!kVec], inv[k][0], inv[k][!kVec], w[k]);
+        fine[k] = q8_codes(x, scale[k][0], scale[k][kA == kNarrow], inv[k][0], inv[k][kA == kNarrow], w[k]);
         all = all && fine[k];
     }
     if (all) return;
@@ -428,16 +460,16 @@ __device__ __forceinline__ void make_codes(const Raw<T> (&raw)[N], const float (
         widen<T>(raw[k], v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f2_unpack(v[j], x[2 * j], x[2 * j + 1]);
-        w[k] = q8_codes_near(x, scale[k][0], scale[k][!kVec], inv[k][0], inv[k][!kVec]);
+        w[k] = q8_codes_near(x, scale[k][0], scale[k][kA == kNarrow], inv[k][0], inv[k][kA == kNarrow]);
     }
 }
 
 // Write a chunk's codes and scales into a checkpoint row.
-template <bool kVec>
-__device__ __forceinline__ void store_codes(uint8_t* row, const CkptShape& s, const Cols<kVec>& c,
+template <int kA>
+__device__ __forceinline__ void store_codes(uint8_t* row, const CkptShape& s, const Cols<kA>& c,
                                             uint32_t lane, uint2 w, const float (&scale)[2]) {
     const uint32_t block = c.c0 >> 7;
-    if constexpr (kVec) {
+    if constexpr (kA != kNarrow) {
         if (c.c0 < s.code_bytes) *reinterpret_cast<uint2*>(row + c.c0) = w;
         if ((lane & 15u) == 0 && block < s.blocks)
             *reinterpret_cast<float*>(row + s.code_bytes + 4u * block) = scale[0];
@@ -456,7 +488,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const CkptShape& s, co
 // Codes and scales of N chunks of a row, the chunks of `at` .. (missing columns hold zeros);
 // every lane of the warp calls it. Lane 2k + b divides for block b of chunk k: two divisions for
 // all the scales and their reciprocals.
-template <typename T, bool kVec, int N>
+template <typename T, int kA, int N>
 __device__ __forceinline__ void save_chunks(uint8_t* row, const CkptShape& s, uint32_t at,
                                             uint32_t stride, uint32_t lane,
                                             const Raw<T> (&raw)[N]) {
@@ -464,7 +496,7 @@ __device__ __forceinline__ void save_chunks(uint8_t* row, const CkptShape& s, ui
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         uint32_t a[2];
-        block_amax<T, kVec>(raw[k], lane, a);
+        block_amax<T, kA>(raw[k], lane, a);
         if (lane == 2 * k) mine = a[0];
         if (lane == 2 * k + 1) mine = a[1];
     }
@@ -472,19 +504,19 @@ __device__ __forceinline__ void save_chunks(uint8_t* row, const CkptShape& s, ui
     float scale[N][2], inv[N][2];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int from = 2 * k + (kVec ? lane >> 4 : 0);
+        const int from = 2 * k + (kA != kNarrow ? lane >> 4 : 0);
         scale[k][0] = __shfl_sync(0xffffffffu, own, from);
         inv[k][0] = __shfl_sync(0xffffffffu, own_inv, from);
-        if (!kVec) {
+        if (kA == kNarrow) {
             scale[k][1] = __shfl_sync(0xffffffffu, own, from + 1);
             inv[k][1] = __shfl_sync(0xffffffffu, own_inv, from + 1);
         }
     }
     uint2 w[N];
-    make_codes<T, kVec, N>(raw, scale, inv, w);
+    make_codes<T, kA, N>(raw, scale, inv, w);
 #pragma unroll
     for (int k = 0; k < N; ++k)
-        store_codes<kVec>(row, s, Cols<kVec>(at + k * stride, lane, s.cols), lane, w[k], scale[k]);
+        store_codes<kA>(row, s, Cols<kA>(at + k * stride, lane, s.cols), lane, w[k], scale[k]);
 }
 
 // Zeros behind a row's scales (at most seven words).
@@ -500,10 +532,11 @@ __device__ __forceinline__ void grid_launch_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Whether a matrix's rows all start on a 16-byte boundary.
+// How the rows of a matrix of `cols` columns can be moved.
 template <typename T>
-bool rows_aligned(const Mat& m) {
-    return aligned16(m.p) && m.ld % (16 / sizeof(T)) == 0;
+Access access_of(const void* p, uint64_t ld, uint32_t cols) {
+    if (!aligned16(p) || ld % (16 / sizeof(T)) != 0) return kNarrow;
+    return cols % 8 == 0 ? kWide : kTail;
 }
 
 template <typename K, typename... A>

@@ -34,21 +34,26 @@ inline CkptShape ckpt_shape(uint64_t cols) {
     return s;
 }
 
+// Rows `pitch` bytes apart: a matrix, or a checkpoint's records. The boundary's calls keep row
+// numbers and pitches below 2^31, so that an address is one multiply-add.
+struct Rows {
+    void* p;
+    uint32_t pitch;
+};
+
 // A boundary's operands (null where absent).
 struct JoinArgs {
-    uint64_t rows;
-    uint32_t cols;
+    uint32_t rows, cols;
     int post, pre;                 // zero_norm
     float post_eps, pre_eps, rs, bs;
-    uint64_t gate_rows;
-    Mat gate, x, h;
-    const uint8_t *x_ckpt, *h_ckpt;
+    uint32_t gate_rows;
+    Rows gate, x, h;
+    bool x_codes, h_codes;         // x, h are checkpoints
     const void *post_w, *post_b, *pre_w, *pre_b;
     // forward
-    Mat y, u;
-    uint8_t *save_y, *save_h;
-    // backward (x and x_ckpt hold the saved y there)
-    Mat dy, du, dx, dh, dgate;
+    Rows y, u, save_y, save_h;
+    // backward (x holds the saved y there)
+    Rows dy, du, dx, dh, dgate;
     void *dpost_w, *dpost_b, *dpre_w, *dpre_b;
     int has_branch, accumulate;
     CkptShape ck;

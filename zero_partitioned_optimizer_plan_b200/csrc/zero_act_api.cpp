@@ -68,12 +68,14 @@ zero_status check_ckpt_call(uint64_t rows, uint64_t cols, int dtype, const void*
     return ZERO_OK;
 }
 
+// The boundary's calls keep row numbers and row pitches (bytes) in 32 bits.
+constexpr uint64_t kMaxRows = 1ull << 31;
+
 // The description's own rules (no buffers but the gate and the vectors).
 zero_status check_desc(const zero_block_desc* d) {
     if (!d || !dtype_ok(d->dtype) || !norm_ok(d->post_norm) || !norm_ok(d->pre_norm))
         return ZERO_EINVAL;
-    if (d->cols > ZERO_JOIN_MAX_COLS || d->rows > kMaxBytes / (4 * ZERO_JOIN_MAX_COLS))
-        return ZERO_EINVAL;
+    if (d->cols > ZERO_JOIN_MAX_COLS || d->rows >= kMaxRows) return ZERO_EINVAL;
     if (!std::isfinite(d->post_eps) || d->post_eps < 0 || !std::isfinite(d->pre_eps) ||
         d->pre_eps < 0 || !std::isfinite(d->residual_scale) || !std::isfinite(d->branch_scale))
         return ZERO_EINVAL;
@@ -94,6 +96,7 @@ struct Buffers {
     Span s[kMax];
     bool out[kMax];
     int n = 0;
+    uint64_t max_pitch = kMaxBytes;
     zero_status st = ZERO_OK;
 
     void add(const Span& sp, uint64_t align, bool is_out) {
@@ -104,7 +107,7 @@ struct Buffers {
     }
     void mat(const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uint64_t es, bool is_out) {
         if (!p) return;
-        if (!shape_ok(rows, cols, ld, es)) {
+        if (!shape_ok(rows, cols, ld, es) || ld * es >= max_pitch) {
             st = ZERO_EINVAL;
             return;
         }
@@ -127,6 +130,7 @@ struct Buffers {
 
 void add_desc(Buffers& b, const zero_block_desc* d) {
     const uint64_t es = elem(d->dtype), vb = d->cols * es;
+    b.max_pitch = kMaxRows;
     b.mat(d->gate, gate_count(d), d->cols, d->ldg, es, false);
     b.add(vec_span(d->post_w, vb), es, false);
     b.add(vec_span(d->post_b, vb), es, false);
@@ -134,9 +138,19 @@ void add_desc(Buffers& b, const zero_block_desc* d) {
     b.add(vec_span(d->pre_b, vb), es, false);
 }
 
+Rows rows_of(const zero_block_desc* d, const void* p, uint64_t ld) {
+    return Rows{const_cast<void*>(p), (uint32_t)(ld * elem(d->dtype))};
+}
+
+// A matrix or a checkpoint.
+Rows source(const zero_block_desc* d, const void* p, uint64_t ld, const uint8_t* ck) {
+    if (ck) return Rows{const_cast<uint8_t*>(ck), (uint32_t)ZERO_CKPT_ROW_BYTES(d->cols)};
+    return rows_of(d, p, ld);
+}
+
 JoinArgs join_args(const zero_block_desc* d) {
     JoinArgs a = {};
-    a.rows = d->rows;
+    a.rows = (uint32_t)d->rows;
     a.cols = (uint32_t)d->cols;
     a.post = d->post_norm;
     a.pre = d->pre_norm;
@@ -144,8 +158,8 @@ JoinArgs join_args(const zero_block_desc* d) {
     a.pre_eps = d->pre_eps;
     a.rs = d->residual_scale;
     a.bs = d->branch_scale;
-    a.gate_rows = d->gate_rows;
-    a.gate = Mat{const_cast<void*>(d->gate), d->ldg};
+    a.gate_rows = (uint32_t)(d->gate_rows < d->rows ? d->gate_rows : d->rows);
+    a.gate = rows_of(d, d->gate, d->ldg);
     a.post_w = d->post_w;
     a.post_b = d->post_b;
     a.pre_w = d->pre_w;
@@ -259,22 +273,21 @@ zero_status zero_block_join(const zero_block_desc* desc, const void* x, uint64_t
     st = b.check(y, x);
     if (st != ZERO_OK) return st;
     JoinArgs a = join_args(desc);
-    a.x = mat(x, ldx);
-    a.x_ckpt = x_ckpt;
-    a.h = mat(h, ldh);
-    a.h_ckpt = h_ckpt;
-    a.y = mat(y, ldy);
-    a.u = mat(u, ldu);
-    a.save_y = save_y;
-    a.save_h = save_h;
+    a.x = source(desc, x, ldx, x_ckpt);
+    a.x_codes = x_ckpt != nullptr;
+    a.h = source(desc, h, ldh, h_ckpt);
+    a.h_codes = h_ckpt != nullptr;
+    a.y = rows_of(desc, y, ldy);
+    a.u = rows_of(desc, u, ldu);
+    a.save_y = source(desc, nullptr, 0, save_y);
+    a.save_h = source(desc, nullptr, 0, save_h);
     a.has_branch = branch;
     return from_cuda(launch_join(a, desc->dtype, (cudaStream_t)stream));
 }
 
 zero_status zero_block_join_backward_workspace(uint64_t rows, uint64_t cols, uint64_t gate_rows,
                                                uint64_t* bytes) {
-    if (!bytes || cols > ZERO_JOIN_MAX_COLS || rows > kMaxBytes / (4 * ZERO_JOIN_MAX_COLS))
-        return ZERO_EINVAL;
+    if (!bytes || cols > ZERO_JOIN_MAX_COLS || rows >= kMaxRows) return ZERO_EINVAL;
     *bytes = join_workspace(rows, cols, gate_rows);
     return ZERO_OK;
 }
@@ -327,15 +340,15 @@ zero_status zero_block_join_backward(const zero_block_desc* desc, int has_branch
     st = b.check(dx, dy);
     if (st != ZERO_OK) return st;
     JoinArgs a = join_args(desc);
-    a.x = mat(y, ldy);
-    a.x_ckpt = y_ckpt;
-    a.h = mat(h, ldh);
-    a.h_ckpt = h_ckpt;
-    a.dy = mat(dy, lddy);
-    a.du = mat(du, lddu);
-    a.dx = mat(dx, lddx);
-    a.dh = mat(dh, lddh);
-    a.dgate = mat(dgate, lddg);
+    a.x = source(desc, y, ldy, y_ckpt);
+    a.x_codes = y_ckpt != nullptr;
+    a.h = source(desc, h, ldh, h_ckpt);
+    a.h_codes = h_ckpt != nullptr;
+    a.dy = rows_of(desc, dy, lddy);
+    a.du = rows_of(desc, du, lddu);
+    a.dx = rows_of(desc, dx, lddx);
+    a.dh = rows_of(desc, dh, lddh);
+    a.dgate = rows_of(desc, dgate, lddg);
     a.dpost_w = dpost_w;
     a.dpost_b = dpost_b;
     a.dpre_w = dpre_w;

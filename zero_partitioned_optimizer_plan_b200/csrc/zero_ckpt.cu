@@ -45,8 +45,8 @@ __device__ __forceinline__ Piece first_piece(const Pieces& p) {
     return a;
 }
 
-template <typename T, bool kVec, int kN>
-__global__ void __launch_bounds__(kThreads, kVec && sizeof(T) == 2 ? 7 : 6)
+template <typename T, int kA, int kN>
+__global__ void __launch_bounds__(kThreads, kA != kNarrow && sizeof(T) == 2 ? 7 : 6)
     ckpt_save_kernel(Pieces p, CkptShape s, Mat x, uint8_t* ckpt) {
     grid_wait();
     const uint32_t lane = threadIdx.x & 31;
@@ -56,13 +56,13 @@ __global__ void __launch_bounds__(kThreads, kVec && sizeof(T) == 2 ? 7 : 6)
         Raw<T> raw[kN];
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-            raw[k] = load_raw<T, kVec>(src, Cols<kVec>(i.at * kN + k, lane, s.cols));
-        save_chunks<T, kVec, kN>(row, s, i.at * kN, 1, lane, raw);
+            raw[k] = load_raw<T, kA>(src, Cols<kA>(i.at * kN + k, lane, s.cols));
+        save_chunks<T, kA, kN>(row, s, i.at * kN, 1, lane, raw);
         if (i.at == 0) save_pad(row, s, lane);
     }
 }
 
-template <typename T, bool kVec, int kN>
+template <typename T, int kA, int kN>
 __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(Pieces p, CkptShape s,
                                                              const uint8_t* ckpt, Mat y) {
     grid_wait();
@@ -73,12 +73,12 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(Pieces p, CkptShape
         Raw<T> raw[kN];
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-            raw[k] = load_codes<T, kVec>(row, s, Cols<kVec>(i.at * kN + k, lane, s.cols));
+            raw[k] = load_codes<T, kA>(row, s, Cols<kA>(i.at * kN + k, lane, s.cols));
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
             F8 v;
             widen_codes<T>(raw[k], v);
-            store_raw<T, kVec>(dst, Cols<kVec>(i.at * kN + k, lane, s.cols), narrow<T>(v));
+            store_raw<T, kA>(dst, Cols<kA>(i.at * kN + k, lane, s.cols), narrow<T>(v));
         }
     }
 }
@@ -115,11 +115,15 @@ cudaError_t run(bool save, uint64_t rows, const CkptShape& s, const Mat& m, uint
     unsigned grid = 1;
     const cudaError_t e = split(rows, s, kN, &p, &grid);
     if (e != cudaSuccess) return e;
-    const bool vec = rows_aligned<T>(m);
+    const Access ac = access_of<T>(m.p, m.ld, s.cols);
     if (save)
-        return launch_act(vec ? ckpt_save_kernel<T, true, kN> : ckpt_save_kernel<T, false, kN>,
+        return launch_act(ac == kWide   ? ckpt_save_kernel<T, kWide, kN>
+                          : ac == kTail ? ckpt_save_kernel<T, kTail, kN>
+                                        : ckpt_save_kernel<T, kNarrow, kN>,
                           dim3(grid), kThreads, 0, stream, p, s, m, ckpt);
-    return launch_act(vec ? ckpt_load_kernel<T, true, kN> : ckpt_load_kernel<T, false, kN>,
+    return launch_act(ac == kWide   ? ckpt_load_kernel<T, kWide, kN>
+                      : ac == kTail ? ckpt_load_kernel<T, kTail, kN>
+                                    : ckpt_load_kernel<T, kNarrow, kN>,
                       dim3(grid), kThreads, 0, stream, p, s, (const uint8_t*)ckpt, m);
 }
 

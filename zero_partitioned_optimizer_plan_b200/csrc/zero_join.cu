@@ -16,9 +16,9 @@ namespace {
 // forward
 // ---------------------------------------------------------------------------------------------
 // z - mean (LayerNorm; missing columns stay 0) and 1/deviation of the team's row.
-template <bool kVec, int G>
+template <int kA, int G>
 __device__ __forceinline__ float centre(Team& t, int kind, float eps, float inv_cols,
-                                        const Cols<kVec> (&c)[G], F8 (&z)[G]) {
+                                        const Cols<kA> (&c)[G], F8 (&z)[G]) {
     float s[2];
     if (kind == ZERO_NORM_LAYER) {
         s[0] = s[1] = 0.0f;
@@ -30,7 +30,7 @@ __device__ __forceinline__ float centre(Team& t, int kind, float eps, float inv_
         for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) z[g][k] = f2_add(z[g][k], m);
-            clear_missing<kVec>(c[g], z[g]);
+            clear_missing<kA>(c[g], z[g]);
         }
     }
     s[0] = s[1] = 0.0f;
@@ -41,46 +41,43 @@ __device__ __forceinline__ float centre(Team& t, int kind, float eps, float inv_
 }
 
 // z*r*w + b.
-template <typename T, bool kVec>
-__device__ __forceinline__ void scale_shift(const Cols<kVec>& c, float r, const void* w,
+template <typename T, int kA>
+__device__ __forceinline__ void scale_shift(const Cols<kA>& c, float r, const void* w,
                                             const void* b, F8& z) {
     F8 wv;
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], both(r));
     if (w) {
-        load_vec<T, kVec>(w, 1.0f, c, wv);
+        load_vec<T, kA>(w, 1.0f, c, wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], wv[k]);
     }
     if (b) {
-        load_vec<T, kVec>(b, 0.0f, c, wv);
+        load_vec<T, kA>(b, 0.0f, c, wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_add(z[k], wv[k]);
     }
 }
 
 // Checkpoint of a warp's chunks; many or 32-bit values one chunk after the other (registers).
-template <typename T, bool kVec, int G>
+template <typename T, int kA, int G>
 __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint32_t at,
                                          uint32_t stride, uint32_t lane, const Raw<T> (&raw)[G]) {
     if constexpr (sizeof(T) == 2 && G <= 2) {
-        save_chunks<T, kVec, G>(row, s, at, stride, lane, raw);
+        save_chunks<T, kA, G>(row, s, at, stride, lane, raw);
     } else {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const Raw<T> one[1] = {raw[g]};
-            save_chunks<T, kVec, 1>(row, s, at + g * stride, stride, lane, one);
+            save_chunks<T, kA, 1>(row, s, at + g * stride, stride, lane, one);
         }
     }
 }
 
-// Warps of a CTA at most. Four chunks of 32-bit values per lane need 255 registers; rows beyond
-// eight such warps are shared by the CTAs of a cluster.
-template <typename T, int G>
-constexpr int forward_warps() { return sizeof(T) * G == 16 ? 8 : kMaxWarps; }
+constexpr int kForwardWarps = 8;   // of a CTA; rows that need more are shared by a cluster
 
-template <typename T, bool kVec, int G>
-__global__ void __launch_bounds__(32 * forward_warps<T, G>(), 1)
+template <typename T, int kA, int G>
+__global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 8 ? 2 : 1)
     join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
     const uint32_t warp = threadIdx.x >> 5, team = warp / warps, teams = (blockDim.x >> 5) / warps;
@@ -89,48 +86,48 @@ __global__ void __launch_bounds__(32 * forward_warps<T, G>(), 1)
     Team t{part, threadIdx.x & 31u, warp - team * warps, team * warps, warps, ctas, rank, team + 1,
            0};
     const uint32_t first = rank * warps + t.warp, step = warps * ctas;   // this warp's chunks
-    const uint64_t cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
-    Cols<kVec> c[G];
+    const uint32_t cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
+    Cols<kA> c[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) c[g] = Cols<kVec>(g * step + first, t.lane, p.cols);
+    for (int g = 0; g < G; ++g) c[g] = Cols<kA>(g * step + first, t.lane, p.cols);
     grid_wait();
-    if (ctas > 1) team_barrier(t);   // every CTA is there before the first remote store
-    for (uint64_t r = cluster * teams + team; r < p.rows; r += clusters * teams) {
+    if (ctas > 1) cluster_barrier();   // every CTA is there before the first remote store
+    for (uint32_t r = cluster * teams + team; r < p.rows; r += clusters * teams) {
         Raw<T> rx[G], rh[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            rx[g] = load_row<T, kVec>(p.x, p.x_ckpt, p.ck, r, c[g]);
-            if (p.has_branch) rh[g] = load_row<T, kVec>(p.h, p.h_ckpt, p.ck, r, c[g]);
+            rx[g] = load_row<T, kA>(p.x, p.x_codes, p.ck, r, c[g]);
+            if (p.has_branch) rh[g] = load_row<T, kA>(p.h, p.h_codes, p.ck, r, c[g]);
         }
-        if (p.save_h) {
-            uint8_t* row = p.save_h + r * p.ck.row_bytes;
-            save_all<T, kVec, G>(row, p.ck, first, step, t.lane, rh);
+        if (p.save_h.p) {
+            uint8_t* row = row_of<uint8_t>(p.save_h, r);
+            save_all<T, kA, G>(row, p.ck, first, step, t.lane, rh);
             if (first == 0) save_pad(row, p.ck, t.lane);
         }
         F8 y[G];
         if (p.has_branch) {
             F8 h[G];
 #pragma unroll
-            for (int g = 0; g < G; ++g) widen_row<T>(rh[g], p.h_ckpt != nullptr, h[g]);
+            for (int g = 0; g < G; ++g) widen_row<T>(rh[g], p.h_codes, h[g]);
             if (p.post != ZERO_NORM_NONE) {
-                const float hr = centre<kVec, G>(t, p.post, p.post_eps, inv_cols, c, h);
+                const float hr = centre<kA, G>(t, p.post, p.post_eps, inv_cols, c, h);
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    scale_shift<T, kVec>(c[g], hr, p.post_w, p.post_b, h[g]);
+                    scale_shift<T, kA>(c[g], hr, p.post_w, p.post_b, h[g]);
             }
             if (p.gate_rows) {
-                const T* gate = (const T*)p.gate.p + row_over(r, p.gate_rows) * p.gate.ld;
+                const T* gate = row_of<T>(p.gate, r / p.gate_rows);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     F8 gv;
-                    widen<T>(load_raw<T, kVec>(gate, c[g]), gv);
+                    widen<T>(load_raw<T, kA>(gate, c[g]), gv);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) h[g][k] = f2_mul(h[g][k], gv[k]);
                 }
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                widen_row<T>(rx[g], p.x_ckpt != nullptr, y[g]);
+                widen_row<T>(rx[g], p.x_codes, y[g]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     y[g][k] = f2_fma(both(p.bs), h[g][k], f2_mul(both(p.rs), y[g][k]));
@@ -138,78 +135,67 @@ __global__ void __launch_bounds__(32 * forward_warps<T, G>(), 1)
         } else {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                widen_row<T>(rx[g], p.x_ckpt != nullptr, y[g]);
+                widen_row<T>(rx[g], p.x_codes, y[g]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[g][k] = f2_mul(both(p.rs), y[g][k]);
             }
         }
-        if (p.y.p || p.save_y) {
+        if (p.y.p || p.save_y.p) {
             Raw<T> ry[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 ry[g] = narrow<T>(y[g]);
-                if (p.y.p) store_raw<T, kVec>((T*)p.y.p + r * p.y.ld, c[g], ry[g]);
+                if (p.y.p) store_raw<T, kA>(row_of<T>(p.y, r), c[g], ry[g]);
             }
-            if (p.save_y) {
-                uint8_t* row = p.save_y + r * p.ck.row_bytes;
-#pragma unroll
-                for (int g = 0; g < G; ++g)   // a post bias may have filled missing columns
-                    if (c[g].mask != 0xffu) {
-                        F8 z;
-                        widen<T>(ry[g], z);
-                        clear_missing<kVec>(c[g], z);
-                        ry[g] = narrow<T>(z);
-                    }
-                save_all<T, kVec, G>(row, p.ck, first, step, t.lane, ry);
+            if (p.save_y.p) {
+                uint8_t* row = row_of<uint8_t>(p.save_y, r);
+                save_all<T, kA, G>(row, p.ck, first, step, t.lane, ry);
                 if (first == 0) save_pad(row, p.ck, t.lane);
             }
         }
         if (p.u.p) {
-            const float yr = centre<kVec, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
+            const float yr = centre<kA, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                scale_shift<T, kVec>(c[g], yr, p.pre_w, p.pre_b, y[g]);
-                store_raw<T, kVec>((T*)p.u.p + r * p.u.ld, c[g], narrow<T>(y[g]));
+                scale_shift<T, kA>(c[g], yr, p.pre_w, p.pre_b, y[g]);
+                store_raw<T, kA>(row_of<T>(p.u, r), c[g], narrow<T>(y[g]));
             }
         }
     }
-    if (ctas > 1) team_barrier(t);   // no CTA leaves while another may still store into it
+    if (ctas > 1) cluster_barrier();   // no CTA leaves while another may still store into it
 }
 
-template <typename T, bool kVec, int G>
-cudaError_t run_forward(const JoinArgs& a, uint32_t warps, int sms, cudaStream_t stream) {
-    uint32_t ctas = 1;
-    while ((warps + ctas - 1) / ctas > (uint32_t)forward_warps<T, G>()) ctas *= 2;
+template <typename T, int kA, int G>
+cudaError_t run_forward(const JoinArgs& a, int sms, cudaStream_t stream) {
+    uint32_t warps = (chunks_of(a.cols) + G - 1) / G, ctas = 1;
+    while ((warps + ctas - 1) / ctas > (uint32_t)kForwardWarps) ctas *= 2;
     warps = (warps + ctas - 1) / ctas;
     const uint32_t teams = ctas == 1 && warps < 4 ? 4 / warps : 1;
-    const uint64_t clusters = (a.rows + teams - 1) / teams, cap = (uint64_t)sms * 32 / ctas;
-    return launch_clusters(join_kernel<T, kVec, G>,
-                           (unsigned)(clusters < cap ? clusters : cap), ctas, 32 * warps * teams,
-                           stream, a, warps, ctas, 1.0f / (float)a.cols);
+    const uint64_t clusters = ((uint64_t)a.rows + teams - 1) / teams, cap = (uint64_t)sms * 32 / ctas;
+    return launch_clusters(join_kernel<T, kA, G>, (unsigned)(clusters < cap ? clusters : cap), ctas,
+                           32 * warps * teams, 0, stream, a, warps, ctas, 1.0f / (float)a.cols);
 }
 
-// Warps and chunks per lane of a row: as few warps as registers allow (one up to 1024 columns:
-// no exchange between warps), but one chunk per warp where there are too few rows to fill the
-// device anyway.
-template <typename T, bool kVec>
+// Chunks per lane: two, so that the work per row that does not grow with the columns is shared by
+// more of them; one where a row is short, has an odd few chunks, or where there are too few rows
+// to fill the device anyway (one token: 4.0 us of 2048 columns, a third less than with two);
+// four for rows that would otherwise need a cluster.
+template <typename T, int kA>
 cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
     DevInfo di;
     const cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
     const uint32_t chunks = chunks_of(a.cols);
-    if (chunks <= kMaxWarps && a.rows <= (uint64_t)di.sms)
-        return run_forward<T, kVec, 1>(a, chunks, di.sms, stream);
-    if (chunks == 1) return run_forward<T, kVec, 1>(a, 1, di.sms, stream);
-    if (chunks == 2) return run_forward<T, kVec, 2>(a, 1, di.sms, stream);
-    if (chunks <= 4) return run_forward<T, kVec, 4>(a, 1, di.sms, stream);
-    if (chunks <= 16) return run_forward<T, kVec, 2>(a, (chunks + 1) / 2, di.sms, stream);
-    return run_forward<T, kVec, 4>(a, (chunks + 3) / 4, di.sms, stream);
+    if (chunks <= 1 || chunks == 3 || (chunks <= kForwardWarps && a.rows <= (uint32_t)di.sms))
+        return run_forward<T, kA, 1>(a, di.sms, stream);
+    if (chunks <= 2 * kForwardWarps) return run_forward<T, kA, 2>(a, di.sms, stream);
+    return run_forward<T, kA, 4>(a, di.sms, stream);
 }
 
 template <typename T>
 cudaError_t run_join(const JoinArgs& a, cudaStream_t stream) {
-    return all_aligned<T>(a) ? run_forward_any<T, true>(a, stream)
-                             : run_forward_any<T, false>(a, stream);
+    return all_access<T>(a) == kWide ? run_forward_any<T, kWide>(a, stream)
+                                     : run_forward_any<T, kNarrow>(a, stream);
 }
 
 }  // namespace

@@ -25,11 +25,11 @@ constexpr int kMaxParts = 148;         // clusters that leave partial column sum
 struct BackGeom {
     uint32_t warps, ctas, teams;   // warps of a CTA per row, CTAs per row, rows a CTA has in hand
     uint32_t clusters;
-    uint64_t group_rows, parts, part_rows, units;
+    uint32_t group_rows, parts, part_rows, units;
     float inv_cols;
 };
 
-BackGeom back_geom(uint64_t rows, uint64_t cols, uint64_t group_rows, uint32_t most_warps,
+BackGeom back_geom(uint32_t rows, uint64_t cols, uint32_t group_rows, uint32_t most_warps,
                    uint32_t sms) {
     BackGeom g = {};
     const uint32_t chunks = chunks_of(cols);
@@ -37,16 +37,16 @@ BackGeom back_geom(uint64_t rows, uint64_t cols, uint64_t group_rows, uint32_t m
     while ((chunks + g.ctas - 1) / g.ctas > most_warps) g.ctas *= 2;
     g.warps = (chunks + g.ctas - 1) / g.ctas;
     g.teams = g.ctas > 1 ? 1 : most_warps / g.warps;
-    uint64_t clusters = sms / g.ctas;
-    if (clusters > kMaxParts) clusters = kMaxParts;
-    const uint64_t useful = (rows + g.teams - 1) / g.teams;
+    uint32_t clusters = sms / g.ctas;
+    if (clusters > (uint32_t)kMaxParts) clusters = kMaxParts;
+    const uint32_t useful = (rows + g.teams - 1) / g.teams;
     if (clusters > useful) clusters = useful;
     if (clusters < 1) clusters = 1;
-    g.clusters = (uint32_t)clusters;
+    g.clusters = clusters;
     g.group_rows = group_rows && group_rows < rows ? group_rows : rows;
     if (g.group_rows) {
-        const uint64_t groups = (rows + g.group_rows - 1) / g.group_rows;
-        uint64_t parts = (uint64_t)g.clusters * g.teams / groups;
+        const uint32_t groups = (rows + g.group_rows - 1) / g.group_rows;
+        uint32_t parts = g.clusters * g.teams / groups;
         if (parts < 1) parts = 1;
         g.part_rows = (g.group_rows + parts - 1) / parts;
         g.parts = (g.group_rows + g.part_rows - 1) / g.part_rows;
@@ -56,28 +56,32 @@ BackGeom back_geom(uint64_t rows, uint64_t cols, uint64_t group_rows, uint32_t m
     return g;
 }
 
-// A team's place in its rows.
+// A team's place in its rows; row == end: no more.
 struct Walk {
-    uint64_t unit, row, end;
-    __device__ __forceinline__ void open(const BackGeom& g, uint64_t rows) {
-        while (unit < g.units) {
-            const uint64_t group = row_over(unit, g.parts), part = unit - group * g.parts;
-            const uint64_t first = group * g.group_rows;
-            uint64_t last = first + g.group_rows < rows ? first + g.group_rows : rows;
-            row = first + part * g.part_rows;
+    uint32_t unit, row, end;
+    __device__ __forceinline__ explicit Walk(uint32_t first) : unit(first), row(0), end(0) {}
+    __device__ __forceinline__ void open(const BackGeom& g, uint32_t rows) {
+        for (; unit < g.units; unit += g.clusters * g.teams) {
+            const uint32_t group = unit / g.parts, first = group * g.group_rows;
+            const uint32_t last = first + min(g.group_rows, rows - first);
+            row = first + (unit - group * g.parts) * g.part_rows;
             end = row + g.part_rows < last ? row + g.part_rows : last;
             if (row < end) return;
-            unit += (uint64_t)g.clusters * g.teams;
         }
+        row = end = 0;
     }
-    // to the next row; true if it belongs to another unit
-    __device__ __forceinline__ bool next(const BackGeom& g, uint64_t rows) {
+    // to the next row; true if it is another unit's (or none)
+    __device__ __forceinline__ bool next(const BackGeom& g, uint32_t rows) {
         if (++row < end) return false;
-        unit += (uint64_t)g.clusters * g.teams;
+        unit += g.clusters * g.teams;
         open(g, rows);
         return true;
     }
 };
+
+constexpr uint32_t kDepth = 4;     // rows a team has on the way (kWide)
+constexpr uint32_t kOps = 5;       // y, du, h, dy, gate
+constexpr uint32_t kVectors = 3;   // pre_w, post_w, post_b
 
 template <typename T>
 __device__ __forceinline__ void put_sum(void* p, uint64_t at, float s, bool add) {
@@ -94,8 +98,8 @@ __host__ __device__ __forceinline__ uint64_t vector_partials(uint32_t cols) {
 template <typename T>
 constexpr int back_warps() { return sizeof(T) == 4 ? 8 : 16; }   // registers: 255 and 128
 
-template <typename T, bool kVec, bool kPost, bool kGate>
-__global__ void __launch_bounds__(32 * back_warps<T>())
+template <typename T, int kA, bool kPost, bool kGate>
+__global__ void __launch_bounds__(32 * back_warps<T>(), 1)
     join_back_kernel(const __grid_constant__ JoinArgs p, const __grid_constant__ BackGeom g,
                      float* ws) {
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
@@ -109,9 +113,9 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
     const uint32_t cluster = g.ctas > 1 ? blockIdx.x / g.ctas : blockIdx.x;
     Team t{part, threadIdx.x & 31u, warp - team * g.warps, team * g.warps, g.warps, g.ctas, rank,
            team + 1, 0};
-    const Cols<kVec> c(rank * g.warps + t.warp, t.lane, p.cols);
+    const Cols<kA> c(rank * g.warps + t.warp, t.lane, p.cols);
     const bool has_du = p.du.p != nullptr;
-    const bool y_codes = p.x_ckpt != nullptr, h_codes = p.h_ckpt != nullptr;
+    const bool y_codes = p.x_codes, h_codes = p.h_codes;
     const bool pre_layer = has_du && p.pre == ZERO_NORM_LAYER;
     const bool post_layer = kPost && p.post == ZERO_NORM_LAYER;
     F8 sum_pw = {}, sum_pb = {}, sum_qw = {}, sum_qb = {};
@@ -121,31 +125,95 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
             held[0][warp][j][t.lane] = held[kSharedBias][warp][j][t.lane] = 0.0f;
     }
     grid_wait();
-    if (g.ctas > 1) team_barrier(t);   // every CTA of the cluster is there before the first store
+    if (g.ctas > 1) cluster_barrier();   // every CTA of the cluster is there before the first store
 
-    Walk at{(uint64_t)cluster * g.teams + team, 0, 0};
-    at.open(g, p.rows);
-    Raw<T> ry, rh, rdu;
-    auto fetch = [&](uint64_t r) {
-        if (has_du) {
-            ry = load_row<T, kVec>(p.x, p.x_ckpt, p.ck, r, c);
-            rdu = load_raw<T, kVec>((const T*)p.du.p + r * p.du.ld, c);
+    // kWide: rows and vectors in this thread's slots of shared memory. kNarrow: the next row's
+    // loads in registers.
+    extern __shared__ uint4 dynamic[];
+    const Slots<T> slots{smem_addr(dynamic) + threadIdx.x * 16u, blockDim.x};
+    Raw<T> ry, rh, rdu, rdy;
+    auto fetch = [&](uint32_t r, uint32_t stage) {
+        if constexpr (kA == kWide) {
+            const uint32_t n = kVectors + stage * kOps;
+            if (has_du) {
+                slots.copy_row(n, p.x, y_codes, p.ck, r, c);
+                slots.copy(n + 1, row_of<T>(p.du, r), c);
+            }
+            if (kPost || kGate) slots.copy_row(n + 2, p.h, h_codes, p.ck, r, c);
+            if (p.dy.p) slots.copy(n + 3, row_of<T>(p.dy, r), c);
+            if (p.gate_rows) slots.copy(n + 4, row_of<T>(p.gate, r / p.gate_rows), c);
+        } else {
+            if (has_du) {
+                ry = load_row<T, kA>(p.x, y_codes, p.ck, r, c);
+                rdu = load_raw<T, kA>(row_of<T>(p.du, r), c);
+            }
+            if (kPost || kGate) rh = load_row<T, kA>(p.h, h_codes, p.ck, r, c);
         }
-        if (kPost || kGate) rh = load_row<T, kVec>(p.h, p.h_ckpt, p.ck, r, c);
     };
-    if (at.unit < g.units) fetch(at.row);
-    while (at.unit < g.units) {
-        const uint64_t r = at.row, unit = at.unit;
-        Raw<T> rdy;   // not needed before the first exchange: no load ahead
-        if (p.dy.p) rdy = load_raw<T, kVec>((const T*)p.dy.p + r * p.dy.ld, c);
-        F8 y, h, du, gu, gy;
-        if (has_du) {
-            widen_row<T>(ry, y_codes, y);
-            widen<T>(rdu, du);
+    auto vector = [&](int n, const void* v, float none, F8& out) {
+        if (kA == kWide && v)
+            widen<T>(slots.get(n), out);
+        else
+            load_vec<T, kA>(v, none, c, out);
+    };
+    if constexpr (kA == kWide) {
+        if (!c.any())
+            for (uint32_t n = 0; n < kVectors + kDepth * kOps; ++n) slots.clear(n);
+        const void* const vectors[kVectors] = {p.pre_w, p.post_w, p.post_b};
+#pragma unroll
+        for (int n = 0; n < (int)kVectors; ++n)
+            if (vectors[n]) slots.put(n, load_raw<T, kA>((const T*)vectors[n], c));
+    }
+    constexpr uint32_t kLoads = kA == kWide ? kDepth : 1;   // rows ahead
+    Walk in(cluster * g.teams + team), at = in;
+    in.open(g, p.rows);
+    at.open(g, p.rows);
+#pragma unroll
+    for (uint32_t k = 0; k < kLoads; ++k) {
+        if (in.row < in.end) {
+            fetch(in.row, k);
+            in.next(g, p.rows);
         }
-        if (kPost || kGate) widen_row<T>(rh, h_codes, h);
+        if (kA == kWide) copy_commit();
+    }
+    uint32_t stage = 0;
+    while (at.row < at.end) {
+        const uint32_t r = at.row, unit = at.unit;
+        F8 y, h, du, gu, gy, gate;
+        if constexpr (kA == kWide) {
+            copy_wait<kLoads - 1>();
+            const uint32_t n = kVectors + stage * kOps;
+            if (has_du) {
+                widen_row<T>(slots.get_row(n, y_codes), y_codes, y);
+                widen<T>(slots.get(n + 1), du);
+            }
+            if (kPost || kGate) widen_row<T>(slots.get_row(n + 2, h_codes), h_codes, h);
+            if (p.dy.p) {
+                widen<T>(slots.get(n + 3), gy);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) gy[k] = 0;
+            }
+            if (p.gate_rows) widen<T>(slots.get(n + 4), gate);
+        } else {
+            if (has_du) {
+                widen_row<T>(ry, y_codes, y);
+                widen<T>(rdu, du);
+            }
+            if (kPost || kGate) widen_row<T>(rh, h_codes, h);
+            if (p.dy.p) rdy = load_raw<T, kA>(row_of<T>(p.dy, r), c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) gy[k] = 0;
+        }
         const bool turn = at.next(g, p.rows);
-        if (at.unit < g.units) fetch(at.row);   // the next row, while this one is worked on
+        if (in.row < in.end) {   // into the slots just read
+            fetch(in.row, stage);
+            in.next(g, p.rows);
+        }
+        if (kA == kWide) {
+            copy_commit();
+            stage = stage + 1 == kDepth ? 0 : stage + 1;
+        }
 
         if (pre_layer || post_layer) {
             float s[2] = {pre_layer ? sum8(y) : 0.0f, post_layer ? sum8(h) : 0.0f};
@@ -154,13 +222,13 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
                 const uint64_t m = both(__fmul_rn(s[0], -g.inv_cols));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[k] = f2_add(y[k], m);
-                clear_missing<kVec>(c, y);
+                clear_missing<kA>(c, y);
             }
             if (post_layer) {
                 const uint64_t m = both(__fmul_rn(s[1], -g.inv_cols));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) h[k] = f2_add(h[k], m);
-                clear_missing<kVec>(c, h);
+                clear_missing<kA>(c, h);
             }
         }
         float hr = 1.0f, yr = 0.0f, m1 = 0.0f, m2 = 0.0f;
@@ -168,7 +236,7 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (has_du) {
                 F8 w;
-                load_vec<T, kVec>(p.pre_w, 1.0f, c, w);
+                vector(0, p.pre_w, 1.0f, w);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) gu[k] = f2_mul(du[k], w[k]);
                 s[0] = dot8(y, y);
@@ -185,12 +253,7 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
                 m2 = __fmul_rn(__fmul_rn(s[2], yr), g.inv_cols);
             }
         }
-        if (p.dy.p) {
-            widen<T>(rdy, gy);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) gy[k] = 0;
-        }
+        if (kA == kNarrow && p.dy.p) widen<T>(rdy, gy);
         if (has_du) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -200,13 +263,13 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
                 const uint64_t d = f2_fma(yh, both(-m2), f2_add(gu[k], both(-m1)));
                 gy[k] = f2_fma(both(yr), d, gy[k]);
             }
-            if (pre_layer) clear_missing<kVec>(c, gy);
+            if (pre_layer) clear_missing<kA>(c, gy);
         }
         if (p.dx.p) {
             F8 dx;
 #pragma unroll
             for (int k = 0; k < 4; ++k) dx[k] = f2_mul(both(p.rs), gy[k]);
-            store_raw<T, kVec>((T*)p.dx.p + r * p.dx.ld, c, narrow<T>(dx));
+            store_raw<T, kA>(row_of<T>(p.dx, r), c, narrow<T>(dx));
         }
         if (p.has_branch && (kPost || kGate || p.dh.p)) {
             F8 b;   // t = bs*gate*gy
@@ -219,8 +282,8 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
             }
             if (kGate) {
                 F8 w;
-                load_vec<T, kVec>(kPost ? p.post_w : nullptr, 1.0f, c, w);
-                load_vec<T, kVec>(kPost ? p.post_b : nullptr, 0.0f, c, v);
+                vector(1, kPost ? p.post_w : nullptr, 1.0f, w);
+                vector(2, kPost ? p.post_b : nullptr, 0.0f, v);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float* sum = &held[0][warp][2 * k][t.lane];
@@ -230,13 +293,13 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
                 }
             }
             if (p.gate_rows) {
-                widen<T>(load_raw<T, kVec>((const T*)p.gate.p +
-                                               row_over(r, p.gate_rows) * p.gate.ld, c), v);
+                if (kA == kNarrow)
+                    widen<T>(load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c), gate);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) b[k] = f2_mul(b[k], v[k]);
+                for (int k = 0; k < 4; ++k) b[k] = f2_mul(b[k], gate[k]);
             }
             if (kPost) {
-                load_vec<T, kVec>(p.post_w, 1.0f, c, v);
+                vector(1, p.post_w, 1.0f, v);
                 float s[2];
                 F8 gt;
 #pragma unroll
@@ -260,23 +323,23 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
                     for (int k = 0; k < 4; ++k)
                         gt[k] = f2_mul(both(hr),
                                        f2_fma(h[k], both(-n2), f2_add(gt[k], both(-n1))));
-                    store_raw<T, kVec>((T*)p.dh.p + r * p.dh.ld, c, narrow<T>(gt));
+                    store_raw<T, kA>(row_of<T>(p.dh, r), c, narrow<T>(gt));
                 }
             } else if (p.dh.p) {
-                store_raw<T, kVec>((T*)p.dh.p + r * p.dh.ld, c, narrow<T>(b));
+                store_raw<T, kA>(row_of<T>(p.dh, r), c, narrow<T>(b));
             }
         }
         if (kGate && turn) {   // the unit's part of its gate row's gradient
-            const uint64_t group = row_over(unit, g.parts);
+            const uint32_t group = unit / g.parts;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float f = held[0][warp][j][t.lane];
                 held[0][warp][j][t.lane] = 0.0f;
                 if (!(c.mask >> j & 1u)) continue;
                 if (g.parts > 1)
-                    ws[vector_partials(p.cols) + unit * p.cols + c.at(j)] = f;
+                    ws[vector_partials(p.cols) + (uint64_t)unit * p.cols + c.at(j)] = f;
                 else
-                    put_sum<T>(p.dgate.p, group * p.dgate.ld + c.at(j), f,
+                    put_sum<T>(row_of<T>(p.dgate, group), c.at(j), f,
                                p.accumulate & ZERO_ACC_GATE);
             }
         }
@@ -310,7 +373,7 @@ __global__ void __launch_bounds__(32 * back_warps<T>())
                 put_sum<T>(outs[k], c.at(j), v, p.accumulate & ZERO_ACC_PARAMS);
         }
     }
-    if (g.ctas > 1) team_barrier(t);   // no CTA leaves while another may still store into it
+    if (g.ctas > 1) cluster_barrier();   // no CTA leaves while another may still store into it
 }
 
 // Column sums from the workspace: 32 columns by 16 rows of partial sums per CTA. blockIdx.y < 4:
@@ -330,16 +393,16 @@ __global__ void __launch_bounds__(32 * kSumRows)
     if (!out || (k < 4 && !vectors)) return;
     const uint64_t stride = k < 4 ? 4ull * p.cols : p.cols;
     const float* src = k < 4 ? ws + (uint64_t)k * p.cols
-                             : ws + vector_partials(p.cols) + (k - 4) * g.parts * p.cols;
-    uint64_t n = p.rows ? g.clusters : 0;
+                             : ws + vector_partials(p.cols) + (uint64_t)(k - 4) * g.parts * p.cols;
+    uint32_t n = p.rows ? g.clusters : 0;
     if (k >= 4) {   // the last gate row may be shorter: parts that have rows
-        const uint64_t left = p.rows - (k - 4) * g.group_rows;
+        const uint32_t left = p.rows - (k - 4) * g.group_rows;
         n = ((left < g.group_rows ? left : g.group_rows) + g.part_rows - 1) / g.part_rows;
     }
     float s = 0.0f;
     if (c < p.cols) {
 #pragma unroll 4
-        for (uint64_t i = ry; i < n; i += kSumRows) s = __fadd_rn(s, src[i * stride + c]);
+        for (uint32_t i = ry; i < n; i += kSumRows) s = __fadd_rn(s, src[i * stride + c]);
     }
     part[ry][cx] = s;
     __syncthreads();
@@ -350,24 +413,31 @@ __global__ void __launch_bounds__(32 * kSumRows)
     if (k < 4)
         put_sum<T>(out, c, v, p.accumulate & ZERO_ACC_PARAMS);
     else
-        put_sum<T>(out, (uint64_t)(k - 4) * p.dgate.ld + c, v, p.accumulate & ZERO_ACC_GATE);
+        put_sum<T>(row_of<T>(p.dgate, k - 4), c, v, p.accumulate & ZERO_ACC_GATE);
 }
 
-template <typename T, bool kVec, bool kPost, bool kGate>
+template <typename T, int kA, bool kPost, bool kGate>
 cudaError_t run_back_kernel(const JoinArgs& a, const BackGeom& g, float* ws,
                             cudaStream_t stream) {
-    return launch_clusters(join_back_kernel<T, kVec, kPost, kGate>, g.clusters, g.ctas,
-                           32 * g.warps * g.teams, stream, a, g, ws);
+    auto kernel = join_back_kernel<T, kA, kPost, kGate>;
+    const unsigned threads = 32 * g.warps * g.teams;
+    const size_t smem = kA == kWide ? (size_t)(kVectors + kDepth * kOps) * 8 * sizeof(T) * threads : 0;
+    if (kA == kWide) {
+        const cudaError_t e = allow_smem(kernel, (size_t)(kVectors + kDepth * kOps) * 8 * sizeof(T) *
+                                                     32 * back_warps<T>());
+        if (e != cudaSuccess) return e;
+    }
+    return launch_clusters(kernel, g.clusters, g.ctas, threads, smem, stream, a, g, ws);
 }
 
-template <typename T, bool kVec>
+template <typename T, int kA>
 cudaError_t run_back_any(const JoinArgs& a, const BackGeom& g, float* ws, cudaStream_t stream) {
     const bool post = a.post != ZERO_NORM_NONE && (a.dh.p || a.dgate.p || a.dpost_w || a.dpost_b);
     if (post)
-        return a.dgate.p ? run_back_kernel<T, kVec, true, true>(a, g, ws, stream)
-                         : run_back_kernel<T, kVec, true, false>(a, g, ws, stream);
-    return a.dgate.p ? run_back_kernel<T, kVec, false, true>(a, g, ws, stream)
-                     : run_back_kernel<T, kVec, false, false>(a, g, ws, stream);
+        return a.dgate.p ? run_back_kernel<T, kA, true, true>(a, g, ws, stream)
+                         : run_back_kernel<T, kA, true, false>(a, g, ws, stream);
+    return a.dgate.p ? run_back_kernel<T, kA, false, true>(a, g, ws, stream)
+                     : run_back_kernel<T, kA, false, false>(a, g, ws, stream);
 }
 
 template <typename T>
@@ -381,13 +451,13 @@ cudaError_t run_join_back(const JoinArgs& a, float* ws, cudaStream_t stream) {
     const bool vectors = vec && (g.clusters > 1 || a.rows == 0);
     const bool split = vectors || (a.dgate.p && g.parts > 1);
     if (a.rows) {
-        e = all_aligned<T>(a) ? run_back_any<T, true>(a, g, split ? ws : nullptr, stream)
-                              : run_back_any<T, false>(a, g, split ? ws : nullptr, stream);
+        e = all_access<T>(a) == kWide ? run_back_any<T, kWide>(a, g, split ? ws : nullptr, stream)
+                                      : run_back_any<T, kNarrow>(a, g, split ? ws : nullptr, stream);
         if (e != cudaSuccess) return e;
     }
     if (!split) return cudaSuccess;
-    const uint64_t gates = a.dgate.p && g.parts > 1 ? g.units / g.parts : 0;
-    return launch_act(join_vectors_kernel<T>, dim3((a.cols + 31) / 32, (unsigned)(4 + gates)),
+    const uint32_t gates = a.dgate.p && g.parts > 1 ? g.units / g.parts : 0;
+    return launch_act(join_vectors_kernel<T>, dim3((a.cols + 31) / 32, 4 + gates),
                       32 * kSumRows, 0, stream, a, g, vectors, (const float*)ws);
 }
 
@@ -401,7 +471,9 @@ uint64_t join_workspace(uint64_t rows, uint64_t cols, uint64_t gate_rows) {
     if (gate_rows && rows) {
         uint64_t most = 0;
         for (const uint32_t warps : {8u, 16u}) {
-            const BackGeom g = back_geom(rows, cols, gate_rows, warps, kMaxParts);
+            const BackGeom g = back_geom((uint32_t)rows, cols,
+                                         (uint32_t)(gate_rows < rows ? gate_rows : rows), warps,
+                                         kMaxParts);
             if (g.parts > 1 && g.units > most) most = g.units;
         }
         floats += most * cols;
