@@ -308,12 +308,7 @@ __device__ __forceinline__ void load_vec(const void* p, float none, const Cols<k
 // Zero the columns that do not exist.
 template <int kA>
 __device__ __forceinline__ void clear_missing(const Cols<kA>& c, F8& v) {
-    if (kA == kWide) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = c.any() ? v[k] : 0;
-        return;
-    }
-    if (c.mask == 0xffu) return;
+    if (c.whole()) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float a, b;

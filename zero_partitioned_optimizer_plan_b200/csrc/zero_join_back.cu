@@ -29,13 +29,14 @@ struct BackGeom {
     float inv_cols;
 };
 
-BackGeom back_geom(uint32_t rows, uint64_t cols, uint32_t group_rows, uint32_t most_warps,
-                   uint32_t sms) {
+// lanes_of: chunks of 256 columns per lane (G); most_warps: warps of a CTA.
+BackGeom back_geom(uint32_t rows, uint64_t cols, uint32_t group_rows, uint32_t lane_chunks,
+                   uint32_t most_warps, uint32_t sms) {
     BackGeom g = {};
-    const uint32_t chunks = chunks_of(cols);
+    const uint32_t pieces = (chunks_of(cols) + lane_chunks - 1) / lane_chunks;
     g.ctas = 1;
-    while ((chunks + g.ctas - 1) / g.ctas > most_warps) g.ctas *= 2;
-    g.warps = (chunks + g.ctas - 1) / g.ctas;
+    while ((pieces + g.ctas - 1) / g.ctas > most_warps) g.ctas *= 2;
+    g.warps = (pieces + g.ctas - 1) / g.ctas;
     g.teams = g.ctas > 1 ? 1 : most_warps / g.warps;
     uint32_t clusters = sms / g.ctas;
     if (clusters > (uint32_t)kMaxParts) clusters = kMaxParts;
@@ -55,6 +56,27 @@ BackGeom back_geom(uint32_t rows, uint64_t cols, uint32_t group_rows, uint32_t m
     g.inv_cols = 1.0f / (float)cols;
     return g;
 }
+
+// The shape of one instantiation. A lane holds G chunks (256 columns per warp) of each matrix and
+// the column sums of up to four vectors in registers: one 16-bit chunk takes 128 of them (16 warps
+// per SM), two take 168 without a norm after the block (12 warps) and else, as 32-bit ones do, up
+// to 255 (8 warps).
+template <typename T, bool kPost, bool kGate, int G>
+struct BackShape {
+    static constexpr bool kHeavy = kPost || kGate;
+    static constexpr int kWarps = sizeof(T) == 4 || (G == 2 && kHeavy) ? 8 : G == 2 ? 12 : 16;
+    static constexpr uint32_t kOps = kHeavy ? 5 : 4;       // y, du, dy, gate, h
+    static constexpr uint32_t kVectors = kHeavy ? 3 : 1;   // pre_w, post_w, post_b
+    static constexpr uint32_t kDepth = G == 2 && !kHeavy ? 3 : 4;   // rows on the way
+    static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
+    static constexpr size_t kThreadBytes = (size_t)kSlots * 8 * sizeof(T);
+    // the gate's column sums, and with a norm after the block that norm's bias sums too, live in
+    // shared memory
+    static constexpr int kHeld = kPost && kGate ? 2 : 1;
+    static constexpr size_t kBytes = kThreadBytes * 32 * kWarps +
+                                     (size_t)(kGate ? kHeld * G : 1) * kWarps * 1024 + 4096;
+    static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
+};
 
 // A team's place in its rows; row == end: no more.
 struct Walk {
@@ -79,10 +101,6 @@ struct Walk {
     }
 };
 
-constexpr uint32_t kDepth = 4;     // rows a team has on the way (kWide)
-constexpr uint32_t kOps = 5;       // y, du, h, dy, gate
-constexpr uint32_t kVectors = 3;   // pre_w, post_w, post_b
-
 template <typename T>
 __device__ __forceinline__ void put_sum(void* p, uint64_t at, float s, bool add) {
     T* d = (T*)p + at;
@@ -95,34 +113,36 @@ __host__ __device__ __forceinline__ uint64_t vector_partials(uint32_t cols) {
     return (uint64_t)kMaxParts * 4 * cols;
 }
 
-template <typename T>
-constexpr int back_warps() { return sizeof(T) == 4 ? 8 : 16; }   // registers: 255 and 128
-
-template <typename T, int kA, bool kPost, bool kGate>
-__global__ void __launch_bounds__(32 * back_warps<T>(), 1)
+template <typename T, int kA, bool kPost, bool kGate, int G>
+__global__ void __launch_bounds__(32 * BackShape<T, kPost, kGate, G>::kWarps, 1)
     join_back_kernel(const __grid_constant__ JoinArgs p, const __grid_constant__ BackGeom g,
                      float* ws) {
+    using S = BackShape<T, kPost, kGate, G>;
+    constexpr bool kSharedBias = S::kHeld == 2;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
-    // the gate's column sums, and with a norm after the block that norm's bias sums too: beside
-    // them the registers do not suffice. At the end the teams' sums meet here.
-    constexpr bool kSharedBias = kPost && kGate;
-    __shared__ float held[kSharedBias ? 2 : 1][back_warps<T>()][8][32];
+    // column sums beside the registers; at the end the teams' sums meet in the first of them
+    __shared__ float held[S::kHeld][kGate ? G : 1][S::kWarps][8][32];
     const uint32_t warp = threadIdx.x >> 5, team = warp / g.warps;
     uint32_t rank = 0;
     if (g.ctas > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const uint32_t cluster = g.ctas > 1 ? blockIdx.x / g.ctas : blockIdx.x;
     Team t{part, threadIdx.x & 31u, warp - team * g.warps, team * g.warps, g.warps, g.ctas, rank,
            team + 1, 0};
-    const Cols<kA> c(rank * g.warps + t.warp, t.lane, p.cols);
+    Cols<kA> c[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+        c[i] = Cols<kA>((i * g.ctas + rank) * g.warps + t.warp, t.lane, p.cols);
     const bool has_du = p.du.p != nullptr;
     const bool y_codes = p.x_codes, h_codes = p.h_codes;
     const bool pre_layer = has_du && p.pre == ZERO_NORM_LAYER;
     const bool post_layer = kPost && p.post == ZERO_NORM_LAYER;
-    F8 sum_pw = {}, sum_pb = {}, sum_qw = {}, sum_qb = {};
+    F8 sum_pw[G] = {}, sum_pb[G] = {}, sum_qw[G] = {}, sum_qb[G] = {};
     if (kGate) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            held[0][warp][j][t.lane] = held[kSharedBias][warp][j][t.lane] = 0.0f;
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                held[0][i][warp][j][t.lane] = held[kSharedBias][i][warp][j][t.lane] = 0.0f;
     }
     grid_wait();
     if (g.ctas > 1) cluster_barrier();   // every CTA of the cluster is there before the first store
@@ -131,40 +151,46 @@ __global__ void __launch_bounds__(32 * back_warps<T>(), 1)
     // loads in registers.
     extern __shared__ uint4 dynamic[];
     const Slots<T> slots{smem_addr(dynamic) + threadIdx.x * 16u, blockDim.x};
-    Raw<T> ry, rh, rdu, rdy;
+    Raw<T> ry[G], rh[G], rdu[G], rdy[G];
     auto fetch = [&](uint32_t r, uint32_t stage) {
-        if constexpr (kA == kWide) {
-            const uint32_t n = kVectors + stage * kOps;
-            if (has_du) {
-                slots.copy_row(n, p.x, y_codes, p.ck, r, c);
-                slots.copy(n + 1, row_of<T>(p.du, r), c);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            if constexpr (kA == kWide) {
+                const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
+                if (has_du) {
+                    slots.copy_row(n, p.x, y_codes, p.ck, r, c[i]);
+                    slots.copy(n + G, row_of<T>(p.du, r), c[i]);
+                }
+                if (p.dy.p) slots.copy(n + 2 * G, row_of<T>(p.dy, r), c[i]);
+                if (p.gate_rows) slots.copy(n + 3 * G, row_of<T>(p.gate, r / p.gate_rows), c[i]);
+                if (kPost || kGate) slots.copy_row(n + 4 * G, p.h, h_codes, p.ck, r, c[i]);
+            } else {
+                if (has_du) {
+                    ry[i] = load_row<T, kA>(p.x, y_codes, p.ck, r, c[i]);
+                    rdu[i] = load_raw<T, kA>(row_of<T>(p.du, r), c[i]);
+                }
+                if (kPost || kGate) rh[i] = load_row<T, kA>(p.h, h_codes, p.ck, r, c[i]);
             }
-            if (kPost || kGate) slots.copy_row(n + 2, p.h, h_codes, p.ck, r, c);
-            if (p.dy.p) slots.copy(n + 3, row_of<T>(p.dy, r), c);
-            if (p.gate_rows) slots.copy(n + 4, row_of<T>(p.gate, r / p.gate_rows), c);
-        } else {
-            if (has_du) {
-                ry = load_row<T, kA>(p.x, y_codes, p.ck, r, c);
-                rdu = load_raw<T, kA>(row_of<T>(p.du, r), c);
-            }
-            if (kPost || kGate) rh = load_row<T, kA>(p.h, h_codes, p.ck, r, c);
         }
     };
-    auto vector = [&](int n, const void* v, float none, F8& out) {
+    auto vector = [&](int n, int i, const void* v, float none, F8& out) {
         if (kA == kWide && v)
-            widen<T>(slots.get(n), out);
+            widen<T>(slots.get(n * G + i), out);
         else
-            load_vec<T, kA>(v, none, c, out);
+            load_vec<T, kA>(v, none, c[i], out);
     };
     if constexpr (kA == kWide) {
-        if (!c.any())
-            for (uint32_t n = 0; n < kVectors + kDepth * kOps; ++n) slots.clear(n);
-        const void* const vectors[kVectors] = {p.pre_w, p.post_w, p.post_b};
+        const void* const vectors[3] = {p.pre_w, p.post_w, p.post_b};
 #pragma unroll
-        for (int n = 0; n < (int)kVectors; ++n)
-            if (vectors[n]) slots.put(n, load_raw<T, kA>((const T*)vectors[n], c));
+        for (int i = 0; i < G; ++i) {
+            if (!c[i].any())
+                for (uint32_t n = i; n < S::kSlots; n += G) slots.clear(n);
+#pragma unroll
+            for (int n = 0; n < (int)S::kVectors; ++n)
+                if (vectors[n]) slots.put(n * G + i, load_raw<T, kA>((const T*)vectors[n], c[i]));
+        }
     }
-    constexpr uint32_t kLoads = kA == kWide ? kDepth : 1;   // rows ahead
+    constexpr uint32_t kLoads = kA == kWide ? S::kDepth : 1;   // rows ahead
     Walk in(cluster * g.teams + team), at = in;
     in.open(g, p.rows);
     at.open(g, p.rows);
@@ -179,31 +205,34 @@ __global__ void __launch_bounds__(32 * back_warps<T>(), 1)
     uint32_t stage = 0;
     while (at.row < at.end) {
         const uint32_t r = at.row, unit = at.unit;
-        F8 y, h, du, gu, gy, gate;
-        if constexpr (kA == kWide) {
-            copy_wait<kLoads - 1>();
-            const uint32_t n = kVectors + stage * kOps;
-            if (has_du) {
-                widen_row<T>(slots.get_row(n, y_codes), y_codes, y);
-                widen<T>(slots.get(n + 1), du);
-            }
-            if (kPost || kGate) widen_row<T>(slots.get_row(n + 2, h_codes), h_codes, h);
-            if (p.dy.p) {
-                widen<T>(slots.get(n + 3), gy);
+        F8 y[G], h[G], du[G], gy[G], gate[G];
+        if (kA == kWide) copy_wait<kLoads - 1>();
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            if constexpr (kA == kWide) {
+                const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
+                if (has_du) {
+                    widen_row<T>(slots.get_row(n, y_codes), y_codes, y[i]);
+                    widen<T>(slots.get(n + G), du[i]);
+                }
+                if (p.dy.p) {
+                    widen<T>(slots.get(n + 2 * G), gy[i]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) gy[i][k] = 0;
+                }
+                if (p.gate_rows) widen<T>(slots.get(n + 3 * G), gate[i]);
+                if (kPost || kGate) widen_row<T>(slots.get_row(n + 4 * G, h_codes), h_codes, h[i]);
             } else {
+                if (has_du) {
+                    widen_row<T>(ry[i], y_codes, y[i]);
+                    widen<T>(rdu[i], du[i]);
+                }
+                if (kPost || kGate) widen_row<T>(rh[i], h_codes, h[i]);
+                if (p.dy.p) rdy[i] = load_raw<T, kA>(row_of<T>(p.dy, r), c[i]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) gy[k] = 0;
+                for (int k = 0; k < 4; ++k) gy[i][k] = 0;
             }
-            if (p.gate_rows) widen<T>(slots.get(n + 4), gate);
-        } else {
-            if (has_du) {
-                widen_row<T>(ry, y_codes, y);
-                widen<T>(rdu, du);
-            }
-            if (kPost || kGate) widen_row<T>(rh, h_codes, h);
-            if (p.dy.p) rdy = load_raw<T, kA>(row_of<T>(p.dy, r), c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) gy[k] = 0;
         }
         const bool turn = at.next(g, p.rows);
         if (in.row < in.end) {   // into the slots just read
@@ -212,136 +241,164 @@ __global__ void __launch_bounds__(32 * back_warps<T>(), 1)
         }
         if (kA == kWide) {
             copy_commit();
-            stage = stage + 1 == kDepth ? 0 : stage + 1;
+            stage = stage + 1 == S::kDepth ? 0 : stage + 1;
         }
 
         if (pre_layer || post_layer) {
-            float s[2] = {pre_layer ? sum8(y) : 0.0f, post_layer ? sum8(h) : 0.0f};
-            team_sum<2>(t, s);
-            if (pre_layer) {
-                const uint64_t m = both(__fmul_rn(s[0], -g.inv_cols));
+            float s[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = f2_add(y[k], m);
-                clear_missing<kA>(c, y);
+            for (int i = 0; i < G; ++i) {
+                if (pre_layer) s[0] = __fadd_rn(s[0], sum8(y[i]));
+                if (post_layer) s[1] = __fadd_rn(s[1], sum8(h[i]));
             }
-            if (post_layer) {
-                const uint64_t m = both(__fmul_rn(s[1], -g.inv_cols));
+            team_sum<2>(t, s);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = f2_add(h[k], m);
-                clear_missing<kA>(c, h);
+            for (int i = 0; i < G; ++i) {
+                if (pre_layer) {
+                    const uint64_t m = both(__fmul_rn(s[0], -g.inv_cols));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[i][k] = f2_add(y[i][k], m);
+                    clear_missing<kA>(c[i], y[i]);
+                }
+                if (post_layer) {
+                    const uint64_t m = both(__fmul_rn(s[1], -g.inv_cols));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[i][k] = f2_add(h[i][k], m);
+                    clear_missing<kA>(c[i], h[i]);
+                }
             }
         }
-        float hr = 1.0f, yr = 0.0f, m1 = 0.0f, m2 = 0.0f;
+        float hr = 1.0f;
         if (has_du || kPost) {
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (has_du) {
-                F8 w;
-                vector(0, p.pre_w, 1.0f, w);
+            F8 gu[G];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) gu[k] = f2_mul(du[k], w[k]);
-                s[0] = dot8(y, y);
-                s[1] = sum8(gu);
-                s[2] = dot8(gu, y);
+            for (int i = 0; i < G; ++i) {
+                if (has_du) {
+                    F8 w;
+                    vector(0, i, p.pre_w, 1.0f, w);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) gu[i][k] = f2_mul(du[i][k], w[k]);
+                    s[0] = __fadd_rn(s[0], dot8(y[i], y[i]));
+                    s[1] = __fadd_rn(s[1], sum8(gu[i]));
+                    s[2] = __fadd_rn(s[2], dot8(gu[i], y[i]));
+                }
+                if (kPost) s[3] = __fadd_rn(s[3], dot8(h[i], h[i]));
             }
-            if (kPost) s[3] = dot8(h, h);
             team_sum<4>(t, s);
             if (kPost)
                 hr = __frsqrt_rn(__fadd_rn(__fmul_rn(s[3], g.inv_cols), p.post_eps));
-            if (has_du) {
-                yr = __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], g.inv_cols), p.pre_eps));
-                m1 = pre_layer ? __fmul_rn(s[1], g.inv_cols) : 0.0f;
-                m2 = __fmul_rn(__fmul_rn(s[2], yr), g.inv_cols);
-            }
-        }
-        if (kA == kNarrow && p.dy.p) widen<T>(rdy, gy);
-        if (has_du) {
+            if (kA == kNarrow && p.dy.p) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint64_t yh = f2_mul(y[k], both(yr));
-                sum_pw[k] = f2_fma(du[k], yh, sum_pw[k]);
-                sum_pb[k] = f2_add(sum_pb[k], du[k]);
-                const uint64_t d = f2_fma(yh, both(-m2), f2_add(gu[k], both(-m1)));
-                gy[k] = f2_fma(both(yr), d, gy[k]);
+                for (int i = 0; i < G; ++i) widen<T>(rdy[i], gy[i]);
             }
-            if (pre_layer) clear_missing<kA>(c, gy);
+            if (has_du) {
+                const float yr = __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], g.inv_cols), p.pre_eps));
+                const float m1 = pre_layer ? __fmul_rn(s[1], g.inv_cols) : 0.0f;
+                const float m2 = __fmul_rn(__fmul_rn(s[2], yr), g.inv_cols);
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t yh = f2_mul(y[i][k], both(yr));
+                        sum_pw[i][k] = f2_fma(du[i][k], yh, sum_pw[i][k]);
+                        sum_pb[i][k] = f2_add(sum_pb[i][k], du[i][k]);
+                        const uint64_t d = f2_fma(yh, both(-m2), f2_add(gu[i][k], both(-m1)));
+                        gy[i][k] = f2_fma(both(yr), d, gy[i][k]);
+                    }
+                    if (pre_layer) clear_missing<kA>(c[i], gy[i]);
+                }
+            }
+        } else if (kA == kNarrow && p.dy.p) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) widen<T>(rdy[i], gy[i]);
         }
         if (p.dx.p) {
-            F8 dx;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) dx[k] = f2_mul(both(p.rs), gy[k]);
-            store_raw<T, kA>(row_of<T>(p.dx, r), c, narrow<T>(dx));
+            for (int i = 0; i < G; ++i) {
+                F8 dx;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dx[k] = f2_mul(both(p.rs), gy[i][k]);
+                store_raw<T, kA>(row_of<T>(p.dx, r), c[i], narrow<T>(dx));
+            }
         }
         if (p.has_branch && (kPost || kGate || p.dh.p)) {
-            F8 b;   // t = bs*gate*gy
+            float s[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) b[k] = f2_mul(both(p.bs), gy[k]);
-            F8 v;
-            if (kPost) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = f2_mul(h[k], both(hr));
-            }
-            if (kGate) {
-                F8 w;
-                vector(1, kPost ? p.post_w : nullptr, 1.0f, w);
-                vector(2, kPost ? p.post_b : nullptr, 0.0f, v);
+            for (int i = 0; i < G; ++i) {   // gy becomes t = bs*gate*gy
+                F8 v;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float* sum = &held[0][warp][2 * k][t.lane];
-                    f2_unpack(f2_fma(b[k], kPost ? f2_fma(h[k], w[k], v[k]) : h[k],
-                                     f2_pack(sum[0], sum[32])),
-                              sum[0], sum[32]);
+                    gy[i][k] = f2_mul(both(p.bs), gy[i][k]);
+                    if (kPost) h[i][k] = f2_mul(h[i][k], both(hr));
                 }
-            }
-            if (p.gate_rows) {
-                if (kA == kNarrow)
-                    widen<T>(load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c), gate);
+                if (kGate) {
+                    F8 w;
+                    vector(1, i, kPost ? p.post_w : nullptr, 1.0f, w);
+                    vector(2, i, kPost ? p.post_b : nullptr, 0.0f, v);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) b[k] = f2_mul(b[k], gate[k]);
-            }
-            if (kPost) {
-                vector(1, p.post_w, 1.0f, v);
-                float s[2];
-                F8 gt;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    sum_qw[k] = f2_fma(b[k], h[k], sum_qw[k]);
-                    if (kSharedBias) {
-                        float* sum = &held[kSharedBias][warp][2 * k][t.lane];
-                        f2_unpack(f2_add(b[k], f2_pack(sum[0], sum[32])), sum[0], sum[32]);
-                    } else {
-                        sum_qb[k] = f2_add(sum_qb[k], b[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        float* sum = &held[0][i][warp][2 * k][t.lane];
+                        f2_unpack(f2_fma(gy[i][k], kPost ? f2_fma(h[i][k], w[k], v[k]) : h[i][k],
+                                         f2_pack(sum[0], sum[32])),
+                                  sum[0], sum[32]);
                     }
-                    gt[k] = f2_mul(b[k], v[k]);
                 }
-                if (p.dh.p) {
-                    s[0] = sum8(gt);
-                    s[1] = dot8(gt, h);
+                if (p.gate_rows) {
+                    if (kA == kNarrow)
+                        widen<T>(load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c[i]), gate[i]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) gy[i][k] = f2_mul(gy[i][k], gate[i][k]);
+                }
+                if (kPost) {
+                    vector(1, i, p.post_w, 1.0f, v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        sum_qw[i][k] = f2_fma(gy[i][k], h[i][k], sum_qw[i][k]);
+                        if (kSharedBias) {
+                            float* sum = &held[kSharedBias][i][warp][2 * k][t.lane];
+                            f2_unpack(f2_add(gy[i][k], f2_pack(sum[0], sum[32])), sum[0], sum[32]);
+                        } else {
+                            sum_qb[i][k] = f2_add(sum_qb[i][k], gy[i][k]);
+                        }
+                        gy[i][k] = f2_mul(gy[i][k], v[k]);
+                    }
+                    s[0] = __fadd_rn(s[0], sum8(gy[i]));
+                    s[1] = __fadd_rn(s[1], dot8(gy[i], h[i]));
+                }
+            }
+            if (p.dh.p) {
+                if (kPost) {
                     team_sum<2>(t, s);
                     const float n1 = post_layer ? __fmul_rn(s[0], g.inv_cols) : 0.0f;
                     const float n2 = __fmul_rn(s[1], g.inv_cols);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        gt[k] = f2_mul(both(hr),
-                                       f2_fma(h[k], both(-n2), f2_add(gt[k], both(-n1))));
-                    store_raw<T, kA>(row_of<T>(p.dh, r), c, narrow<T>(gt));
+                    for (int i = 0; i < G; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            gy[i][k] = f2_mul(both(hr), f2_fma(h[i][k], both(-n2),
+                                                               f2_add(gy[i][k], both(-n1))));
                 }
-            } else if (p.dh.p) {
-                store_raw<T, kA>(row_of<T>(p.dh, r), c, narrow<T>(b));
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    store_raw<T, kA>(row_of<T>(p.dh, r), c[i], narrow<T>(gy[i]));
             }
         }
         if (kGate && turn) {   // the unit's part of its gate row's gradient
             const uint32_t group = unit / g.parts;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f = held[0][warp][j][t.lane];
-                held[0][warp][j][t.lane] = 0.0f;
-                if (!(c.mask >> j & 1u)) continue;
-                if (g.parts > 1)
-                    ws[vector_partials(p.cols) + (uint64_t)unit * p.cols + c.at(j)] = f;
-                else
-                    put_sum<T>(row_of<T>(p.dgate, group), c.at(j), f,
-                               p.accumulate & ZERO_ACC_GATE);
-            }
+            for (int i = 0; i < G; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float f = held[0][i][warp][j][t.lane];
+                    held[0][i][warp][j][t.lane] = 0.0f;
+                    if (!(c[i].mask >> j & 1u)) continue;
+                    if (g.parts > 1)
+                        ws[vector_partials(p.cols) + (uint64_t)unit * p.cols + c[i].at(j)] = f;
+                    else
+                        put_sum<T>(row_of<T>(p.dgate, group), c[i].at(j), f,
+                                   p.accumulate & ZERO_ACC_GATE);
+                }
         }
     }
     if (ws) grid_launch_next();
@@ -350,27 +407,30 @@ __global__ void __launch_bounds__(32 * back_warps<T>(), 1)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         if (!outs[k]) continue;
-        const bool there = kSharedBias && k == 1;
-        float(*comb)[8][32] = held[there];
-        __syncthreads();
-        if (!there) {
-            const F8& s = k == 0 ? sum_qw : k == 1 ? sum_qb : k == 2 ? sum_pw : sum_pb;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                f2_unpack(s[j], comb[warp][2 * j][t.lane], comb[warp][2 * j + 1][t.lane]);
+        for (int i = 0; i < G; ++i) {
+            const bool there = kSharedBias && k == 1;
+            float(*comb)[8][32] = held[there][there ? i : 0];
             __syncthreads();
-        }
-        if (team != 0) continue;
+            if (!there) {
+                const F8& s = k == 0 ? sum_qw[i] : k == 1 ? sum_qb[i] : k == 2 ? sum_pw[i] : sum_pb[i];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!(c.mask >> j & 1u)) continue;
-            float v = 0.0f;
-            for (uint32_t i = 0; i < g.teams; ++i)
-                v = __fadd_rn(v, comb[i * g.warps + t.warp][j][t.lane]);
-            if (g.clusters > 1)
-                ws[((uint64_t)cluster * 4 + k) * p.cols + c.at(j)] = v;
-            else
-                put_sum<T>(outs[k], c.at(j), v, p.accumulate & ZERO_ACC_PARAMS);
+                for (int j = 0; j < 4; ++j)
+                    f2_unpack(s[j], comb[warp][2 * j][t.lane], comb[warp][2 * j + 1][t.lane]);
+                __syncthreads();
+            }
+            if (team != 0) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (!(c[i].mask >> j & 1u)) continue;
+                float v = 0.0f;
+                for (uint32_t n = 0; n < g.teams; ++n)
+                    v = __fadd_rn(v, comb[n * g.warps + t.warp][j][t.lane]);
+                if (g.clusters > 1)
+                    ws[((uint64_t)cluster * 4 + k) * p.cols + c[i].at(j)] = v;
+                else
+                    put_sum<T>(outs[k], c[i].at(j), v, p.accumulate & ZERO_ACC_PARAMS);
+            }
         }
     }
     if (g.ctas > 1) cluster_barrier();   // no CTA leaves while another may still store into it
@@ -416,28 +476,41 @@ __global__ void __launch_bounds__(32 * kSumRows)
         put_sum<T>(row_of<T>(p.dgate, k - 4), c, v, p.accumulate & ZERO_ACC_GATE);
 }
 
-template <typename T, int kA, bool kPost, bool kGate>
-cudaError_t run_back_kernel(const JoinArgs& a, const BackGeom& g, float* ws,
-                            cudaStream_t stream) {
-    auto kernel = join_back_kernel<T, kA, kPost, kGate>;
-    const unsigned threads = 32 * g.warps * g.teams;
-    const size_t smem = kA == kWide ? (size_t)(kVectors + kDepth * kOps) * 8 * sizeof(T) * threads : 0;
-    if (kA == kWide) {
-        const cudaError_t e = allow_smem(kernel, (size_t)(kVectors + kDepth * kOps) * 8 * sizeof(T) *
-                                                     32 * back_warps<T>());
-        if (e != cudaSuccess) return e;
-    }
-    return launch_clusters(kernel, g.clusters, g.ctas, threads, smem, stream, a, g, ws);
+// Two chunks per lane of 16-bit rows wider than one (what a row costs beside its columns is then
+// paid by half the warps): 16384 x 2048 fp16 without a norm after the block, 112 us with one.
+template <typename T>
+int lane_chunks(const JoinArgs& a, Access access) {
+    return sizeof(T) == 2 && access == kWide && chunks_of(a.cols) > 1 ? 2 : 1;
 }
 
-template <typename T, int kA>
-cudaError_t run_back_any(const JoinArgs& a, const BackGeom& g, float* ws, cudaStream_t stream) {
+template <typename T, int kA, bool kPost, bool kGate, int G>
+cudaError_t run_back_kernel(const JoinArgs& a, int sms, float* ws, BackGeom* geom,
+                            cudaStream_t stream) {
+    using S = BackShape<T, kPost, kGate, G>;
+    const BackGeom g = back_geom(a.rows, a.cols, a.dgate.p ? a.gate_rows : 0, G, S::kWarps, sms);
+    *geom = g;
+    if (a.rows == 0) return cudaSuccess;
+    auto kernel = join_back_kernel<T, kA, kPost, kGate, G>;
+    const unsigned threads = 32 * g.warps * g.teams;
+    size_t smem = 0;
+    if (kA == kWide) {
+        smem = S::kThreadBytes * threads;
+        const cudaError_t e = allow_smem(kernel, S::kThreadBytes * 32 * S::kWarps);
+        if (e != cudaSuccess) return e;
+    }
+    const bool used = g.clusters > 1 || (a.dgate.p && g.parts > 1);
+    return launch_clusters(kernel, g.clusters, g.ctas, threads, smem, stream, a, g,
+                           used ? ws : (float*)nullptr);
+}
+
+template <typename T, int kA, int G>
+cudaError_t run_back_any(const JoinArgs& a, int sms, float* ws, BackGeom* g, cudaStream_t stream) {
     const bool post = a.post != ZERO_NORM_NONE && (a.dh.p || a.dgate.p || a.dpost_w || a.dpost_b);
     if (post)
-        return a.dgate.p ? run_back_kernel<T, kA, true, true>(a, g, ws, stream)
-                         : run_back_kernel<T, kA, true, false>(a, g, ws, stream);
-    return a.dgate.p ? run_back_kernel<T, kA, false, true>(a, g, ws, stream)
-                     : run_back_kernel<T, kA, false, false>(a, g, ws, stream);
+        return a.dgate.p ? run_back_kernel<T, kA, true, true, G>(a, sms, ws, g, stream)
+                         : run_back_kernel<T, kA, true, false, G>(a, sms, ws, g, stream);
+    return a.dgate.p ? run_back_kernel<T, kA, false, true, G>(a, sms, ws, g, stream)
+                     : run_back_kernel<T, kA, false, false, G>(a, sms, ws, g, stream);
 }
 
 template <typename T>
@@ -445,20 +518,25 @@ cudaError_t run_join_back(const JoinArgs& a, float* ws, cudaStream_t stream) {
     DevInfo di;
     cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
-    const bool vec = a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b;
-    const BackGeom g = back_geom(a.rows, a.cols, a.dgate.p ? a.gate_rows : 0,
-                                 (uint32_t)back_warps<T>(), (uint32_t)di.sms);
-    const bool vectors = vec && (g.clusters > 1 || a.rows == 0);
-    const bool split = vectors || (a.dgate.p && g.parts > 1);
-    if (a.rows) {
-        e = all_access<T>(a) == kWide ? run_back_any<T, kWide>(a, g, split ? ws : nullptr, stream)
-                                      : run_back_any<T, kNarrow>(a, g, split ? ws : nullptr, stream);
-        if (e != cudaSuccess) return e;
+    const Access access = all_access<T>(a);
+    BackGeom g = {};
+    if constexpr (sizeof(T) == 2) {
+        if (lane_chunks<T>(a, access) == 2)
+            e = run_back_any<T, kWide, 2>(a, di.sms, ws, &g, stream);
+        else
+            e = access == kWide ? run_back_any<T, kWide, 1>(a, di.sms, ws, &g, stream)
+                                : run_back_any<T, kNarrow, 1>(a, di.sms, ws, &g, stream);
+    } else {
+        e = access == kWide ? run_back_any<T, kWide, 1>(a, di.sms, ws, &g, stream)
+                            : run_back_any<T, kNarrow, 1>(a, di.sms, ws, &g, stream);
     }
-    if (!split) return cudaSuccess;
-    const uint32_t gates = a.dgate.p && g.parts > 1 ? g.units / g.parts : 0;
-    return launch_act(join_vectors_kernel<T>, dim3((a.cols + 31) / 32, 4 + gates),
-                      32 * kSumRows, 0, stream, a, g, vectors, (const float*)ws);
+    if (e != cudaSuccess) return e;
+    const bool vectors = (a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b) &&
+                         (g.clusters > 1 || a.rows == 0);
+    const uint32_t gates = a.dgate.p && a.rows && g.parts > 1 ? g.units / g.parts : 0;
+    if (!vectors && !gates) return cudaSuccess;
+    return launch_act(join_vectors_kernel<T>, dim3((a.cols + 31) / 32, 4 + gates), 32 * kSumRows,
+                      0, stream, a, g, vectors, (const float*)ws);
 }
 
 }  // namespace
@@ -470,12 +548,13 @@ uint64_t join_workspace(uint64_t rows, uint64_t cols, uint64_t gate_rows) {
     uint64_t floats = vector_partials((uint32_t)cols);
     if (gate_rows && rows) {
         uint64_t most = 0;
-        for (const uint32_t warps : {8u, 16u}) {
-            const BackGeom g = back_geom((uint32_t)rows, cols,
-                                         (uint32_t)(gate_rows < rows ? gate_rows : rows), warps,
-                                         kMaxParts);
-            if (g.parts > 1 && g.units > most) most = g.units;
-        }
+        for (const uint32_t warps : {8u, 12u, 16u})
+            for (const uint32_t chunks : {1u, 2u}) {
+                const BackGeom g = back_geom((uint32_t)rows, cols,
+                                             (uint32_t)(gate_rows < rows ? gate_rows : rows),
+                                             chunks, warps, kMaxParts);
+                if (g.parts > 1 && g.units > most) most = g.units;
+            }
         floats += most * cols;
     }
     return (floats * 4 + 15) / 16 * 16;
