@@ -40,30 +40,40 @@ __device__ __forceinline__ float centre(Team& t, int kind, float eps, float inv_
     return __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], inv_cols), eps));
 }
 
-// z*r*w + b.
+// A norm's weight or bias (not null), from this thread's slot n of shared memory (kWide).
 template <typename T, int kA>
-__device__ __forceinline__ void scale_shift(const Cols<kA>& c, float r, const void* w,
-                                            const void* b, F8& z) {
+__device__ __forceinline__ void vector(const Slots<T>& slots, uint32_t n, const void* v,
+                                       const Cols<kA>& c, F8& out) {
+    if (kA == kWide)
+        widen<T>(slots.get(n), out);
+    else
+        load_vec<T, kA>(v, 0.0f, c, out);
+}
+
+// z*r*w + b; slots n and n + G hold w and b.
+template <typename T, int kA, int G>
+__device__ __forceinline__ void scale_shift(const Slots<T>& slots, uint32_t n, const Cols<kA>& c,
+                                            float r, const void* w, const void* b, F8& z) {
     F8 wv;
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], both(r));
     if (w) {
-        load_vec<T, kA>(w, 1.0f, c, wv);
+        vector<T, kA>(slots, n, w, c, wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], wv[k]);
     }
     if (b) {
-        load_vec<T, kA>(b, 0.0f, c, wv);
+        vector<T, kA>(slots, n + G, b, c, wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_add(z[k], wv[k]);
     }
 }
 
-// Checkpoint of a warp's chunks; many or 32-bit values one chunk after the other (registers).
+// Checkpoint of a warp's chunks; 32-bit values one chunk after the other (registers).
 template <typename T, int kA, int G>
 __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint32_t at,
                                          uint32_t stride, uint32_t lane, const Raw<T> (&raw)[G]) {
-    if constexpr (sizeof(T) == 2 && G <= 2) {
+    if constexpr (sizeof(T) == 2) {
         save_chunks<T, kA, G>(row, s, at, stride, lane, raw);
     } else {
 #pragma unroll
@@ -76,9 +86,19 @@ __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint3
 
 constexpr int kForwardWarps = 8;   // of a CTA; rows that need more are shared by a cluster
 
+// Rows on the way: what lets two CTAs (three of one 16-bit chunk per lane) fit an SM.
+template <typename T, int G>
+struct ForwardShape {
+    static constexpr uint32_t kVectors = 4;   // post_w, post_b, pre_w, pre_b
+    static constexpr uint32_t kOps = 3;       // x, h, gate
+    static constexpr uint32_t kDepth = sizeof(T) * G == 2 ? 4 : sizeof(T) * G == 4 ? 3 : 2;
+    static constexpr size_t kThreadBytes = (size_t)(kVectors + kDepth * kOps) * G * 8 * sizeof(T);
+};
+
 template <typename T, int kA, int G>
-__global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 4 ? 2 : 1)
     join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
+    using S = ForwardShape<T, G>;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
     const uint32_t warp = threadIdx.x >> 5, team = warp / warps, teams = (blockDim.x >> 5) / warps;
     uint32_t rank = 0;
@@ -86,18 +106,67 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 8 ? 2 : 1
     Team t{part, threadIdx.x & 31u, warp - team * warps, team * warps, warps, ctas, rank, team + 1,
            0};
     const uint32_t first = rank * warps + t.warp, step = warps * ctas;   // this warp's chunks
-    const uint32_t cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
+    const uint32_t cluster = blockIdx.x / ctas, stride = gridDim.x / ctas * teams;
     Cols<kA> c[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) c[g] = Cols<kA>(g * step + first, t.lane, p.cols);
     grid_wait();
     if (ctas > 1) cluster_barrier();   // every CTA is there before the first remote store
-    for (uint32_t r = cluster * teams + team; r < p.rows; r += clusters * teams) {
-        Raw<T> rx[G], rh[G];
+
+    extern __shared__ uint4 dynamic[];
+    const Slots<T> slots{smem_addr(dynamic) + threadIdx.x * 16u, blockDim.x};
+    auto fetch = [&](uint32_t r, uint32_t stage) {
+        if constexpr (kA == kWide) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
+                slots.copy_row(n, p.x, p.x_codes, p.ck, r, c[g]);
+                if (p.has_branch) slots.copy_row(n + G, p.h, p.h_codes, p.ck, r, c[g]);
+                if (p.gate_rows) slots.copy(n + 2 * G, row_of<T>(p.gate, r / p.gate_rows), c[g]);
+            }
+        }
+    };
+    uint32_t r = cluster * teams + team, ahead = r, stage = 0;
+    if constexpr (kA == kWide) {
+#pragma unroll
+        for (uint32_t k = 0; k < S::kDepth; ++k) {
+            if (ahead < p.rows) fetch(ahead, k);
+            ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
+            copy_commit();
+        }
+        const void* const vectors[S::kVectors] = {p.post_w, p.post_b, p.pre_w, p.pre_b};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            rx[g] = load_row<T, kA>(p.x, p.x_codes, p.ck, r, c[g]);
-            if (p.has_branch) rh[g] = load_row<T, kA>(p.h, p.h_codes, p.ck, r, c[g]);
+            if (!c[g].any())
+                for (uint32_t n = g; n < (S::kVectors + S::kDepth * S::kOps) * G; n += G)
+                    slots.clear(n);
+#pragma unroll
+            for (int n = 0; n < (int)S::kVectors; ++n)
+                if (vectors[n]) slots.put(n * G + g, load_raw<T, kA>((const T*)vectors[n], c[g]));
+        }
+    }
+    for (; r < p.rows; r = stride < p.rows - r ? r + stride : p.rows) {
+        Raw<T> rx[G], rh[G], rg[G];
+        if (kA == kWide) copy_wait<S::kDepth - 1>();
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if constexpr (kA == kWide) {
+                const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
+                rx[g] = slots.get_row(n, p.x_codes);
+                if (p.has_branch) rh[g] = slots.get_row(n + G, p.h_codes);
+                if (p.gate_rows) rg[g] = slots.get(n + 2 * G);
+            } else {
+                rx[g] = load_row<T, kA>(p.x, p.x_codes, p.ck, r, c[g]);
+                if (p.has_branch) rh[g] = load_row<T, kA>(p.h, p.h_codes, p.ck, r, c[g]);
+                if (p.gate_rows)
+                    rg[g] = load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c[g]);
+            }
+        }
+        if (kA == kWide) {   // the next row into the slots just read
+            if (ahead < p.rows) fetch(ahead, stage);
+            ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
+            copy_commit();
+            stage = stage + 1 == S::kDepth ? 0 : stage + 1;
         }
         if (p.save_h.p) {
             uint8_t* row = row_of<uint8_t>(p.save_h, r);
@@ -113,14 +182,13 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 8 ? 2 : 1
                 const float hr = centre<kA, G>(t, p.post, p.post_eps, inv_cols, c, h);
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    scale_shift<T, kA>(c[g], hr, p.post_w, p.post_b, h[g]);
+                    scale_shift<T, kA, G>(slots, g, c[g], hr, p.post_w, p.post_b, h[g]);
             }
             if (p.gate_rows) {
-                const T* gate = row_of<T>(p.gate, r / p.gate_rows);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     F8 gv;
-                    widen<T>(load_raw<T, kA>(gate, c[g]), gv);
+                    widen<T>(rg[g], gv);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) h[g][k] = f2_mul(h[g][k], gv[k]);
                 }
@@ -157,7 +225,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 8 ? 2 : 1
             const float yr = centre<kA, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                scale_shift<T, kA>(c[g], yr, p.pre_w, p.pre_b, y[g]);
+                scale_shift<T, kA, G>(slots, 2 * G + g, c[g], yr, p.pre_w, p.pre_b, y[g]);
                 store_raw<T, kA>(row_of<T>(p.u, r), c[g], narrow<T>(y[g]));
             }
         }
@@ -166,20 +234,29 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 8 ? 2 : 1
 }
 
 template <typename T, int kA, int G>
-cudaError_t run_forward(const JoinArgs& a, int sms, cudaStream_t stream) {
+cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t stream) {
     uint32_t warps = (chunks_of(a.cols) + G - 1) / G, ctas = 1;
     while ((warps + ctas - 1) / ctas > (uint32_t)kForwardWarps) ctas *= 2;
     warps = (warps + ctas - 1) / ctas;
-    const uint32_t teams = ctas == 1 && warps < 4 ? 4 / warps : 1;
-    const uint64_t clusters = ((uint64_t)a.rows + teams - 1) / teams, cap = (uint64_t)sms * 32 / ctas;
-    return launch_clusters(join_kernel<T, kA, G>, (unsigned)(clusters < cap ? clusters : cap), ctas,
-                           32 * warps * teams, 0, stream, a, warps, ctas, 1.0f / (float)a.cols);
+    const uint32_t teams = ctas == 1 ? kForwardWarps / warps : 1;
+    const unsigned threads = 32 * warps * teams;
+    auto kernel = join_kernel<T, kA, G>;
+    const size_t smem = kA == kWide ? ForwardShape<T, G>::kThreadBytes * threads : 0;
+    int per_sm = 1;
+    const cudaError_t e = resident(kernel, di.dev, threads, smem,
+                                   kA == kWide ? ForwardShape<T, G>::kThreadBytes * 32 * kForwardWarps
+                                               : 0,
+                                   &per_sm);
+    if (e != cudaSuccess) return e;
+    const uint64_t clusters = ((uint64_t)a.rows + teams - 1) / teams;
+    const uint64_t cap = (uint64_t)di.sms * per_sm / ctas;
+    return launch_clusters(kernel, (unsigned)(clusters < cap ? clusters : cap), ctas, threads, smem,
+                           stream, a, warps, ctas, 1.0f / (float)a.cols);
 }
 
 // Chunks per lane: two, so that the work per row that does not grow with the columns is shared by
-// more of them; one where a row is short, has an odd few chunks, or where there are too few rows
-// to fill the device anyway (one token: 4.0 us of 2048 columns, a third less than with two);
-// four for rows that would otherwise need a cluster.
+// more of them; one where a row has one chunk or three, or where there are too few rows to fill
+// the device anyway.
 template <typename T, int kA>
 cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
     DevInfo di;
@@ -187,9 +264,8 @@ cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint32_t chunks = chunks_of(a.cols);
     if (chunks <= 1 || chunks == 3 || (chunks <= kForwardWarps && a.rows <= (uint32_t)di.sms))
-        return run_forward<T, kA, 1>(a, di.sms, stream);
-    if (chunks <= 2 * kForwardWarps) return run_forward<T, kA, 2>(a, di.sms, stream);
-    return run_forward<T, kA, 4>(a, di.sms, stream);
+        return run_forward<T, kA, 1>(a, di, stream);
+    return run_forward<T, kA, 2>(a, di, stream);
 }
 
 template <typename T>

@@ -163,24 +163,32 @@ struct Slots {
     }
 };
 
-// Let a kernel use `smem` bytes of dynamic shared memory on the current device.
+// Let a kernel use up to `most` bytes of dynamic shared memory on device `dev`, and tell how many
+// of its CTAs (threads, smem) an SM holds at once. Asked once per host thread and shape.
 template <typename K>
-cudaError_t allow_smem(K kernel, size_t smem) {
+cudaError_t resident(K kernel, int dev, unsigned threads, size_t smem, size_t most, int* ctas) {
     constexpr int kSlots = 64;
     thread_local struct {
         const void* kernel;
         int dev;
+        unsigned threads;
+        int ctas;
     } known[kSlots];
     thread_local int used = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
     const void* kp = reinterpret_cast<const void*>(kernel);
     for (int i = 0; i < used; ++i)
-        if (known[i].kernel == kp && known[i].dev == dev) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && used < kSlots) known[used++] = {kp, dev};
-    return e;
+        if (known[i].kernel == kp && known[i].dev == dev && known[i].threads == threads) {
+            *ctas = known[i].ctas;
+            return cudaSuccess;
+        }
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)most);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, (int)threads, smem);
+    if (e != cudaSuccess) return e;
+    if (*ctas < 1) return cudaErrorInvalidConfiguration;
+    if (used < kSlots) known[used++] = {kp, dev, threads, *ctas};
+    return cudaSuccess;
 }
 
 // launch_act in clusters of `ctas` CTAs.

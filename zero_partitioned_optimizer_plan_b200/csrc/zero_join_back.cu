@@ -61,20 +61,18 @@ BackGeom back_geom(uint32_t rows, uint64_t cols, uint32_t group_rows, uint32_t l
 // the column sums of up to four vectors in registers: one 16-bit chunk takes 128 of them (16 warps
 // per SM), two take 168 without a norm after the block (12 warps) and else, as 32-bit ones do, up
 // to 255 (8 warps).
-template <typename T, bool kPost, bool kGate, int G>
+template <typename T, int kA, bool kPost, bool kGate, int G>
 struct BackShape {
     static constexpr bool kHeavy = kPost || kGate;
-    static constexpr int kWarps = sizeof(T) == 4 || (G == 2 && kHeavy) ? 8 : G == 2 ? 12 : 16;
+    static constexpr bool kMany = (G == 2 && kHeavy) || (kA == kNarrow && kPost && kGate);
+    static constexpr int kWarps = sizeof(T) == 4 || kMany ? 8 : G == 2 ? 12 : 16;
     static constexpr uint32_t kOps = kHeavy ? 5 : 4;       // y, du, dy, gate, h
     static constexpr uint32_t kVectors = kHeavy ? 3 : 1;   // pre_w, post_w, post_b
     static constexpr uint32_t kDepth = G == 2 && !kHeavy ? 3 : 4;   // rows on the way
     static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
     static constexpr size_t kThreadBytes = (size_t)kSlots * 8 * sizeof(T);
-    // the gate's column sums, and with a norm after the block that norm's bias sums too, live in
-    // shared memory
-    static constexpr int kHeld = kPost && kGate ? 2 : 1;
     static constexpr size_t kBytes = kThreadBytes * 32 * kWarps +
-                                     (size_t)(kGate ? kHeld * G : 1) * kWarps * 1024 + 4096;
+                                     (size_t)(kPost && kGate ? 2 * G : 1) * kWarps * 1024 + 4096;
     static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -114,14 +112,18 @@ __host__ __device__ __forceinline__ uint64_t vector_partials(uint32_t cols) {
 }
 
 template <typename T, int kA, bool kPost, bool kGate, int G>
-__global__ void __launch_bounds__(32 * BackShape<T, kPost, kGate, G>::kWarps, 1)
+__global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps, 1)
     join_back_kernel(const __grid_constant__ JoinArgs p, const __grid_constant__ BackGeom g,
                      float* ws) {
-    using S = BackShape<T, kPost, kGate, G>;
-    constexpr bool kSharedBias = S::kHeld == 2;
+    using S = BackShape<T, kA, kPost, kGate, G>;
+    // With a norm after the block and a gate gradient, sum_qw and sum_qb are those of one gate row
+    // without its gate: bs*gy*hh and bs*gy. Where the gate row ends they give its gradient,
+    // w*sum_qw + b*sum_qb, and, multiplied by the gate, go into the norm's own sums in shared
+    // memory. With a gate gradient alone, sum_qw is bs*gy*h.
+    constexpr bool kBoth = kPost && kGate;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
     // column sums beside the registers; at the end the teams' sums meet in the first of them
-    __shared__ float held[S::kHeld][kGate ? G : 1][S::kWarps][8][32];
+    __shared__ float held[kBoth ? 2 : 1][kBoth ? G : 1][S::kWarps][8][32];
     const uint32_t warp = threadIdx.x >> 5, team = warp / g.warps;
     uint32_t rank = 0;
     if (g.ctas > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -137,12 +139,12 @@ __global__ void __launch_bounds__(32 * BackShape<T, kPost, kGate, G>::kWarps, 1)
     const bool pre_layer = has_du && p.pre == ZERO_NORM_LAYER;
     const bool post_layer = kPost && p.post == ZERO_NORM_LAYER;
     F8 sum_pw[G] = {}, sum_pb[G] = {}, sum_qw[G] = {}, sum_qb[G] = {};
-    if (kGate) {
+    if (kBoth) {
 #pragma unroll
         for (int i = 0; i < G; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                held[0][i][warp][j][t.lane] = held[kSharedBias][i][warp][j][t.lane] = 0.0f;
+                held[0][i][warp][j][t.lane] = held[kBoth][i][warp][j][t.lane] = 0.0f;
     }
     grid_wait();
     if (g.ctas > 1) cluster_barrier();   // every CTA of the cluster is there before the first store
@@ -333,15 +335,10 @@ __global__ void __launch_bounds__(32 * BackShape<T, kPost, kGate, G>::kWarps, 1)
                     if (kPost) h[i][k] = f2_mul(h[i][k], both(hr));
                 }
                 if (kGate) {
-                    F8 w;
-                    vector(1, i, kPost ? p.post_w : nullptr, 1.0f, w);
-                    vector(2, i, kPost ? p.post_b : nullptr, 0.0f, v);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float* sum = &held[0][i][warp][2 * k][t.lane];
-                        f2_unpack(f2_fma(gy[i][k], kPost ? f2_fma(h[i][k], w[k], v[k]) : h[i][k],
-                                         f2_pack(sum[0], sum[32])),
-                                  sum[0], sum[32]);
+                        sum_qw[i][k] = f2_fma(gy[i][k], h[i][k], sum_qw[i][k]);
+                        if (kPost) sum_qb[i][k] = f2_add(sum_qb[i][k], gy[i][k]);
                     }
                 }
                 if (p.gate_rows) {
@@ -354,11 +351,8 @@ __global__ void __launch_bounds__(32 * BackShape<T, kPost, kGate, G>::kWarps, 1)
                     vector(1, i, p.post_w, 1.0f, v);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        sum_qw[i][k] = f2_fma(gy[i][k], h[i][k], sum_qw[i][k]);
-                        if (kSharedBias) {
-                            float* sum = &held[kSharedBias][i][warp][2 * k][t.lane];
-                            f2_unpack(f2_add(gy[i][k], f2_pack(sum[0], sum[32])), sum[0], sum[32]);
-                        } else {
+                        if (!kGate) {
+                            sum_qw[i][k] = f2_fma(gy[i][k], h[i][k], sum_qw[i][k]);
                             sum_qb[i][k] = f2_add(sum_qb[i][k], gy[i][k]);
                         }
                         gy[i][k] = f2_mul(gy[i][k], v[k]);
@@ -387,30 +381,55 @@ __global__ void __launch_bounds__(32 * BackShape<T, kPost, kGate, G>::kWarps, 1)
         if (kGate && turn) {   // the unit's part of its gate row's gradient
             const uint32_t group = unit / g.parts;
 #pragma unroll
-            for (int i = 0; i < G; ++i)
+            for (int i = 0; i < G; ++i) {
+                F8 part_g;
+                if (kPost) {
+                    F8 w, b;
+                    vector(1, i, p.post_w, 1.0f, w);
+                    vector(2, i, p.post_b, 0.0f, b);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        part_g[k] = f2_fma(sum_qw[i][k], w[k], f2_mul(sum_qb[i][k], b[k]));
+                        float* qw = &held[0][i][warp][2 * k][t.lane];
+                        float* qb = &held[kBoth][i][warp][2 * k][t.lane];
+                        f2_unpack(f2_fma(sum_qw[i][k], gate[i][k], f2_pack(qw[0], qw[32])), qw[0],
+                                  qw[32]);
+                        f2_unpack(f2_fma(sum_qb[i][k], gate[i][k], f2_pack(qb[0], qb[32])), qb[0],
+                                  qb[32]);
+                        sum_qw[i][k] = sum_qb[i][k] = 0;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        part_g[k] = sum_qw[i][k];
+                        sum_qw[i][k] = 0;
+                    }
+                }
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f2_unpack(part_g[k], f[2 * k], f[2 * k + 1]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float f = held[0][i][warp][j][t.lane];
-                    held[0][i][warp][j][t.lane] = 0.0f;
                     if (!(c[i].mask >> j & 1u)) continue;
                     if (g.parts > 1)
-                        ws[vector_partials(p.cols) + (uint64_t)unit * p.cols + c[i].at(j)] = f;
+                        ws[vector_partials(p.cols) + (uint64_t)unit * p.cols + c[i].at(j)] = f[j];
                     else
-                        put_sum<T>(row_of<T>(p.dgate, group), c[i].at(j), f,
+                        put_sum<T>(row_of<T>(p.dgate, group), c[i].at(j), f[j],
                                    p.accumulate & ZERO_ACC_GATE);
                 }
+            }
         }
     }
     if (ws) grid_launch_next();
     // the teams' column sums, added in order; to the workspace, or as they are if one CTA had all
     void* const outs[4] = {p.dpost_w, p.dpost_b, p.dpre_w, p.dpre_b};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4; ++k) {   // (held[0] holds the first one until it is done)
         if (!outs[k]) continue;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            const bool there = kSharedBias && k == 1;
-            float(*comb)[8][32] = held[there][there ? i : 0];
+            const bool there = kBoth && k < 2;   // already in shared memory
+            float(*comb)[8][32] = there ? held[k][i] : held[0][0];
             __syncthreads();
             if (!there) {
                 const F8& s = k == 0 ? sum_qw[i] : k == 1 ? sum_qb[i] : k == 2 ? sum_pw[i] : sum_pb[i];
@@ -484,33 +503,34 @@ int lane_chunks(const JoinArgs& a, Access access) {
 }
 
 template <typename T, int kA, bool kPost, bool kGate, int G>
-cudaError_t run_back_kernel(const JoinArgs& a, int sms, float* ws, BackGeom* geom,
+cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, BackGeom* geom,
                             cudaStream_t stream) {
-    using S = BackShape<T, kPost, kGate, G>;
-    const BackGeom g = back_geom(a.rows, a.cols, a.dgate.p ? a.gate_rows : 0, G, S::kWarps, sms);
+    using S = BackShape<T, kA, kPost, kGate, G>;
+    const BackGeom g = back_geom(a.rows, a.cols, a.dgate.p ? a.gate_rows : 0, G, S::kWarps,
+                                 (uint32_t)di.sms);
     *geom = g;
     if (a.rows == 0) return cudaSuccess;
     auto kernel = join_back_kernel<T, kA, kPost, kGate, G>;
     const unsigned threads = 32 * g.warps * g.teams;
-    size_t smem = 0;
-    if (kA == kWide) {
-        smem = S::kThreadBytes * threads;
-        const cudaError_t e = allow_smem(kernel, S::kThreadBytes * 32 * S::kWarps);
-        if (e != cudaSuccess) return e;
-    }
+    const size_t smem = kA == kWide ? S::kThreadBytes * threads : 0;
+    int ctas = 1;
+    const cudaError_t e = resident(kernel, di.dev, threads, smem,
+                                   kA == kWide ? S::kThreadBytes * 32 * S::kWarps : 0, &ctas);
+    if (e != cudaSuccess) return e;
     const bool used = g.clusters > 1 || (a.dgate.p && g.parts > 1);
     return launch_clusters(kernel, g.clusters, g.ctas, threads, smem, stream, a, g,
                            used ? ws : (float*)nullptr);
 }
 
 template <typename T, int kA, int G>
-cudaError_t run_back_any(const JoinArgs& a, int sms, float* ws, BackGeom* g, cudaStream_t stream) {
+cudaError_t run_back_any(const JoinArgs& a, const DevInfo& di, float* ws, BackGeom* g,
+                         cudaStream_t stream) {
     const bool post = a.post != ZERO_NORM_NONE && (a.dh.p || a.dgate.p || a.dpost_w || a.dpost_b);
     if (post)
-        return a.dgate.p ? run_back_kernel<T, kA, true, true, G>(a, sms, ws, g, stream)
-                         : run_back_kernel<T, kA, true, false, G>(a, sms, ws, g, stream);
-    return a.dgate.p ? run_back_kernel<T, kA, false, true, G>(a, sms, ws, g, stream)
-                     : run_back_kernel<T, kA, false, false, G>(a, sms, ws, g, stream);
+        return a.dgate.p ? run_back_kernel<T, kA, true, true, G>(a, di, ws, g, stream)
+                         : run_back_kernel<T, kA, true, false, G>(a, di, ws, g, stream);
+    return a.dgate.p ? run_back_kernel<T, kA, false, true, G>(a, di, ws, g, stream)
+                     : run_back_kernel<T, kA, false, false, G>(a, di, ws, g, stream);
 }
 
 template <typename T>
@@ -522,13 +542,13 @@ cudaError_t run_join_back(const JoinArgs& a, float* ws, cudaStream_t stream) {
     BackGeom g = {};
     if constexpr (sizeof(T) == 2) {
         if (lane_chunks<T>(a, access) == 2)
-            e = run_back_any<T, kWide, 2>(a, di.sms, ws, &g, stream);
+            e = run_back_any<T, kWide, 2>(a, di, ws, &g, stream);
         else
-            e = access == kWide ? run_back_any<T, kWide, 1>(a, di.sms, ws, &g, stream)
-                                : run_back_any<T, kNarrow, 1>(a, di.sms, ws, &g, stream);
+            e = access == kWide ? run_back_any<T, kWide, 1>(a, di, ws, &g, stream)
+                                : run_back_any<T, kNarrow, 1>(a, di, ws, &g, stream);
     } else {
-        e = access == kWide ? run_back_any<T, kWide, 1>(a, di.sms, ws, &g, stream)
-                            : run_back_any<T, kNarrow, 1>(a, di.sms, ws, &g, stream);
+        e = access == kWide ? run_back_any<T, kWide, 1>(a, di, ws, &g, stream)
+                            : run_back_any<T, kNarrow, 1>(a, di, ws, &g, stream);
     }
     if (e != cudaSuccess) return e;
     const bool vectors = (a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b) &&
