@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes as C
 import dataclasses
 import os
+import struct
 from typing import List, Sequence
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libzero.so")
@@ -140,16 +141,6 @@ class ScalerParams(C.Structure):
                 ("growth_interval", C.c_int32)]
 
 
-class BlockDesc(C.Structure):
-    """zero_block_desc: what a block boundary's forward and backward calls share."""
-    _fields_ = [("rows", C.c_uint64), ("cols", C.c_uint64), ("dtype", C.c_int),
-                ("post_norm", C.c_int), ("pre_norm", C.c_int), ("post_eps", C.c_float),
-                ("pre_eps", C.c_float), ("residual_scale", C.c_float),
-                ("branch_scale", C.c_float), ("gate_rows", C.c_uint64), ("gate", C.c_void_p),
-                ("ldg", C.c_uint64), ("post_w", C.c_void_p), ("post_b", C.c_void_p),
-                ("pre_w", C.c_void_p), ("pre_b", C.c_void_p)]
-
-
 @dataclasses.dataclass(frozen=True)
 class AdamHP:
     lr: float = 1e-3
@@ -242,10 +233,10 @@ def _load():
     L.zero_ckpt_wgrad_q8_workspace.argtypes = [u64, u64, u64, P(u64)]
     L.zero_ckpt_wgrad_q8.argtypes = [u64, u64, u64, i32, vp, u64, vp, vp, u64, i32, vp, u64, vp,
                                      vp]
-    L.zero_block_join.argtypes = [P(BlockDesc), vp, u64, vp, vp, u64, vp, vp, u64, vp, u64, vp,
+    L.zero_block_join.argtypes = [C.c_char_p, vp, u64, vp, vp, u64, vp, vp, u64, vp, u64, vp,
                                   vp, vp]
     L.zero_block_join_backward_workspace.argtypes = [u64, u64, u64, P(u64)]
-    L.zero_block_join_backward.argtypes = [P(BlockDesc), i32, vp, u64, vp, vp, u64, vp, vp, u64,
+    L.zero_block_join_backward.argtypes = [C.c_char_p, i32, vp, u64, vp, vp, u64, vp, vp, u64,
                                            vp, u64, vp, u64, vp, u64, vp, u64, vp, vp, vp, vp,
                                            i32, vp, u64, vp]
     # every other entry point returns a zero_status: ctypes' default int restype
@@ -270,10 +261,21 @@ def _ptr(x, elem_size: int | None = None) -> int:
     return int(x)
 
 
+_current_raw_stream = None
+
+
 def _stream(s) -> int:
     if s is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        global _current_raw_stream
+        if _current_raw_stream is None:
+            import torch
+            torch.cuda.current_stream()          # initialises CUDA
+            try:                                 # the handle without a Stream object around it
+                raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+                _current_raw_stream = lambda: raw(device())
+            except AttributeError:
+                _current_raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)
+        return _current_raw_stream()
     if hasattr(s, "cuda_stream"):
         return int(s.cuda_stream)
     return int(s)
@@ -845,32 +847,32 @@ def zero_sched_destroy(s: Sched):
 # ---------------------------------------------------------------------------------------------
 _DTYPE_CODES: dict = {}
 _NORM_CODES = {"none": ZERO_NORM_NONE, "rms": ZERO_NORM_RMS, "layer": ZERO_NORM_LAYER}
-
-
-def _dtype(x) -> int | None:
-    """The zero_dtype of a tensor, None of an address."""
-    if not hasattr(x, "data_ptr"):
-        return None
-    if not _DTYPE_CODES:
-        import torch
-        _DTYPE_CODES.update({torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16,
-                             torch.float32: ZERO_F32})
-    code = _DTYPE_CODES.get(x.dtype)
-    if code is None:
-        raise TypeError(f"expected float16, bfloat16 or float32, got {x.dtype}")
-    return code
+# zero_block_desc: rows, cols, dtype, post_norm, pre_norm, post_eps, pre_eps, residual_scale,
+# branch_scale, gate_rows, gate, ldg, post_w, post_b, pre_w, pre_b
+_BLOCK_DESC = struct.Struct("@QQiiiffff4xQQQQQQQ")
 
 
 def _dtype_of(xs, dtype) -> int:
     """The one zero_dtype of the tensors among xs (`dtype` where all are addresses)."""
+    first = None
     for x in xs:
-        code = _dtype(x)
-        if code is None:
+        t = getattr(x, "dtype", None)
+        if t is None or t is first:
             continue
-        if dtype is None:
-            dtype = code
-        elif code != dtype:
+        if first is not None:
             raise TypeError("tensors of different types in one call")
+        first = t
+    if first is not None:
+        if not _DTYPE_CODES:
+            import torch
+            _DTYPE_CODES.update({torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16,
+                                 torch.float32: ZERO_F32})
+        code = _DTYPE_CODES.get(first)
+        if code is None:
+            raise TypeError(f"expected float16, bfloat16 or float32, got {first}")
+        if dtype is not None and dtype != code:
+            raise TypeError("tensors of another type than dtype")
+        return code
     if dtype is None:
         raise TypeError("dtype is needed where every operand is an address")
     return dtype
@@ -881,29 +883,36 @@ def _mat(x, rows: int, cols: int):
     rows may be strided), (address, stride), or an address of adjacent rows."""
     if x is None:
         return 0, cols
-    if hasattr(x, "data_ptr"):
-        if tuple(x.shape) != (rows, cols):
-            raise TypeError(f"expected a {rows} x {cols} tensor, got {tuple(x.shape)}")
-        s0, s1 = x.stride()
-        if s1 != 1 and cols > 1:
-            raise TypeError("the columns of a matrix must be adjacent")
-        return int(x.data_ptr()), int(s0) if rows > 1 else max(int(s0), cols)
-    if isinstance(x, tuple):
-        return int(x[0]), int(x[1])
-    return int(x), cols
+    try:
+        shape, stride, ptr = x.shape, x.stride(), x.data_ptr()
+    except AttributeError:
+        return (int(x[0]), int(x[1])) if isinstance(x, tuple) else (int(x), cols)
+    if shape != (rows, cols):
+        raise TypeError(f"expected a {rows} x {cols} tensor, got {tuple(shape)}")
+    if stride[1] != 1 and cols > 1:
+        raise TypeError("the columns of a matrix must be adjacent")
+    ld = stride[0]
+    return ptr, ld if rows > 1 or ld > cols else cols
 
 
 def _ckpt(x, rows: int, cols: int) -> int:
-    if x is not None and hasattr(x, "data_ptr") and \
-            x.numel() * x.element_size() < rows * ckpt_row_bytes(cols):
+    if x is None:
+        return 0
+    if hasattr(x, "data_ptr") and x.nbytes < rows * ckpt_row_bytes(cols):
         raise TypeError("checkpoint buffer smaller than rows * ckpt_row_bytes(cols)")
     return _ptr(x, 1)
 
 
 def _vec(x, cols: int) -> int:
-    if x is not None and hasattr(x, "data_ptr") and x.numel() != cols:
-        raise TypeError(f"expected a vector of {cols} values, got {tuple(x.shape)}")
-    return _ptr(x)
+    if x is None:
+        return 0
+    try:
+        n, ptr = x.numel(), x.data_ptr()
+    except AttributeError:
+        return int(x)
+    if n != cols or not x.is_contiguous():
+        raise TypeError(f"expected a contiguous vector of {cols} values, got {tuple(x.shape)}")
+    return ptr
 
 
 def _nbytes(x, given=None) -> int:
@@ -915,15 +924,18 @@ def _nbytes(x, given=None) -> int:
 def zero_ckpt_save_q8(rows: int, cols: int, x, ckpt, dtype: int | None = None, stream=None):
     """x: a rows x cols tensor (rows may be strided), or (address, stride) with dtype."""
     p, ld = _mat(x, rows, cols)
-    _check(_lib.zero_ckpt_save_q8(rows, cols, _dtype_of((x,), dtype), p, ld,
-                                  _ckpt(ckpt, rows, cols), _stream(stream)),
-           "zero_ckpt_save_q8")
+    code = _lib.zero_ckpt_save_q8(rows, cols, _dtype_of((x,), dtype), p, ld,
+                                  _ckpt(ckpt, rows, cols), _stream(stream))
+    if code:
+        raise ZeroError(code, "zero_ckpt_save_q8")
 
 
 def zero_ckpt_load_q8(rows: int, cols: int, ckpt, out, dtype: int | None = None, stream=None):
     p, ld = _mat(out, rows, cols)
-    _check(_lib.zero_ckpt_load_q8(rows, cols, _ckpt(ckpt, rows, cols), _dtype_of((out,), dtype),
-                                  p, ld, _stream(stream)), "zero_ckpt_load_q8")
+    code = _lib.zero_ckpt_load_q8(rows, cols, _ckpt(ckpt, rows, cols), _dtype_of((out,), dtype),
+                                  p, ld, _stream(stream))
+    if code:
+        raise ZeroError(code, "zero_ckpt_load_q8")
 
 
 def zero_ckpt_wgrad_q8_workspace(tokens: int, out_features: int, in_features: int) -> int:
@@ -948,12 +960,15 @@ def zero_ckpt_wgrad_q8(tokens: int, out_features: int, in_features: int, dy, ckp
 
 
 def _block_desc(rows, cols, dtype, post_norm, pre_norm, post_eps, pre_eps, residual_scale,
-                branch_scale, gate, gate_rows, post_w, post_b, pre_w, pre_b) -> BlockDesc:
-    g, ldg = _mat(gate, -(-rows // gate_rows) if gate_rows else 0, cols)
-    return BlockDesc(rows, cols, dtype, _NORM_CODES.get(post_norm, post_norm),
-                     _NORM_CODES.get(pre_norm, pre_norm), post_eps, pre_eps, residual_scale,
-                     branch_scale, gate_rows, g, ldg, _vec(post_w, cols), _vec(post_b, cols),
-                     _vec(pre_w, cols), _vec(pre_b, cols))
+                branch_scale, gate, gate_rows, post_w, post_b, pre_w, pre_b) -> bytes:
+    g, ldg = _mat(gate, -(-rows // gate_rows), cols) if gate_rows else _mat(gate, 0, cols)
+    post_norm = _NORM_CODES.get(post_norm, post_norm)
+    pre_norm = _NORM_CODES.get(pre_norm, pre_norm)
+    if isinstance(post_norm, str) or isinstance(pre_norm, str):
+        raise TypeError(f"norms {post_norm!r}, {pre_norm!r}: none, rms or layer")
+    return _BLOCK_DESC.pack(rows, cols, dtype, post_norm, pre_norm, post_eps, pre_eps,
+                            residual_scale, branch_scale, gate_rows, g, ldg, _vec(post_w, cols),
+                            _vec(post_b, cols), _vec(pre_w, cols), _vec(pre_b, cols))
 
 
 def zero_block_join(rows: int, cols: int, *, x=None, x_ckpt=None, h=None, h_ckpt=None, y=None,
@@ -966,11 +981,16 @@ def zero_block_join(rows: int, cols: int, *, x=None, x_ckpt=None, h=None, h_ckpt
     d = _block_desc(rows, cols, _dtype_of((x, h, y, u, gate, post_w, post_b, pre_w, pre_b), dtype),
                     post_norm, pre_norm, post_eps, pre_eps, residual_scale, branch_scale, gate,
                     gate_rows, post_w, post_b, pre_w, pre_b)
-    _check(_lib.zero_block_join(C.byref(d), *_mat(x, rows, cols), _ckpt(x_ckpt, rows, cols),
-                                *_mat(h, rows, cols), _ckpt(h_ckpt, rows, cols),
-                                *_mat(y, rows, cols), *_mat(u, rows, cols),
+    xp, ldx = _mat(x, rows, cols)
+    hp, ldh = _mat(h, rows, cols)
+    yp, ldy = _mat(y, rows, cols)
+    up, ldu = _mat(u, rows, cols)
+    code = _lib.zero_block_join(d, xp, ldx, _ckpt(x_ckpt, rows, cols), hp, ldh,
+                                _ckpt(h_ckpt, rows, cols), yp, ldy, up, ldu,
                                 _ckpt(save_y, rows, cols), _ckpt(save_h, rows, cols),
-                                _stream(stream)), "zero_block_join")
+                                _stream(stream))
+    if code:
+        raise ZeroError(code, "zero_block_join")
 
 
 def zero_block_join_backward_workspace(rows: int, cols: int, gate_rows: int = 0) -> int:
@@ -996,7 +1016,7 @@ def zero_block_join_backward(rows: int, cols: int, *, y=None, y_ckpt=None, h=Non
                     gate_rows, post_w, post_b, pre_w, pre_b)
     gates = -(-rows // gate_rows) if gate_rows else 0
     _check(_lib.zero_block_join_backward(
-        C.byref(d), 1 if has_branch else 0, *_mat(y, rows, cols), _ckpt(y_ckpt, rows, cols),
+        d, 1 if has_branch else 0, *_mat(y, rows, cols), _ckpt(y_ckpt, rows, cols),
         *_mat(h, rows, cols), _ckpt(h_ckpt, rows, cols), *_mat(dy, rows, cols),
         *_mat(du, rows, cols), *_mat(dx, rows, cols), *_mat(dh, rows, cols),
         *_mat(dgate, gates, cols), _vec(dpost_w, cols), _vec(dpost_b, cols), _vec(dpre_w, cols),
