@@ -770,8 +770,9 @@ zero_status zero_ckpt_load_q8(uint64_t rows, uint64_t cols, const uint8_t* ckpt,
  *               to their elements; 16-byte aligned rows of dy take the tensor-map loads.
  *   ckpt      : the checkpoint of a (tokens rows of in_features columns), 16-byte aligned
  *   workspace : zero_ckpt_wgrad_q8_workspace(...) bytes (may be 0, then NULL is accepted),
- *               16-byte aligned device memory, overwritten; calls that may run at the same time
- *               need workspaces of their own
+ *               16-byte aligned device memory, overwritten: partial sums where a long sum goes
+ *               into few outputs, and an aligned copy of dy where out_features is no multiple of
+ *               8. Calls that may run at the same time need workspaces of their own
  *   d_status  : ZERO_FLAG_TIMEOUT is ORed in if a wait inside the kernel gave up
  * tokens == 0 writes zeros (or leaves dw with accumulate); out_features or in_features == 0
  * launches nothing. Errors: ZERO_EINVAL (null, dtype, a feature count >= 2^30, tokens >= 2^31, a

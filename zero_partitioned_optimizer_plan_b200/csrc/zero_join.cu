@@ -40,30 +40,20 @@ __device__ __forceinline__ float centre(Team& t, int kind, float eps, float inv_
     return __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], inv_cols), eps));
 }
 
-// A norm's weight or bias (not null), from this thread's slot n of shared memory (kWide).
-template <typename T, int kA>
-__device__ __forceinline__ void vector(const Slots<T>& slots, uint32_t n, const void* v,
-                                       const Cols<kA>& c, F8& out) {
-    if (kA == kWide)
-        widen<T>(slots.get(n), out);
-    else
-        load_vec<T, kA>(v, 0.0f, c, out);
-}
-
 // z*r*w + b; slots n and n + G hold w and b.
-template <typename T, int kA, int G>
-__device__ __forceinline__ void scale_shift(const Slots<T>& slots, uint32_t n, const Cols<kA>& c,
-                                            float r, const void* w, const void* b, F8& z) {
+template <typename T, int G>
+__device__ __forceinline__ void scale_shift(const Slots<T>& slots, uint32_t n, float r, bool w,
+                                            bool b, F8& z) {
     F8 wv;
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], both(r));
     if (w) {
-        vector<T, kA>(slots, n, w, c, wv);
+        widen<T>(slots.get(n), wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], wv[k]);
     }
     if (b) {
-        vector<T, kA>(slots, n + G, b, c, wv);
+        widen<T>(slots.get(n + G), wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_add(z[k], wv[k]);
     }
@@ -87,18 +77,19 @@ __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint3
 constexpr int kForwardWarps = 8;   // of a CTA; rows that need more are shared by a cluster
 
 // Rows on the way: what lets two CTAs (three of one 16-bit chunk per lane) fit an SM.
-template <typename T, int G>
+template <typename T, int kA, int G>
 struct ForwardShape {
     static constexpr uint32_t kVectors = 4;   // post_w, post_b, pre_w, pre_b
     static constexpr uint32_t kOps = 3;       // x, h, gate
-    static constexpr uint32_t kDepth = sizeof(T) * G == 2 ? 4 : sizeof(T) * G == 4 ? 3 : 2;
+    static constexpr bool kPipe = piped<T, kA>();
+    static constexpr uint32_t kDepth = !kPipe ? 0 : sizeof(T) * G == 2 ? 4 : sizeof(T) * G == 4 ? 3 : 2;
     static constexpr size_t kThreadBytes = (size_t)(kVectors + kDepth * kOps) * G * 8 * sizeof(T);
 };
 
 template <typename T, int kA, int G>
 __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 4 ? 2 : 1)
     join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
-    using S = ForwardShape<T, G>;
+    using S = ForwardShape<T, kA, G>;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
     const uint32_t warp = threadIdx.x >> 5, team = warp / warps, teams = (blockDim.x >> 5) / warps;
     uint32_t rank = 0;
@@ -115,56 +106,63 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 4 ? 2 : 1
 
     extern __shared__ uint4 dynamic[];
     const Slots<T> slots{smem_addr(dynamic) + threadIdx.x * 16u, blockDim.x};
+    Raw<T> nx[G], nh[G], ng[G];   // the next row's values, where they do not go through slots
     auto fetch = [&](uint32_t r, uint32_t stage) {
-        if constexpr (kA == kWide) {
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
+        for (int g = 0; g < G; ++g) {
+            if constexpr (S::kPipe) {
                 const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
-                slots.copy_row(n, p.x, p.x_codes, p.ck, r, c[g]);
-                if (p.has_branch) slots.copy_row(n + G, p.h, p.h_codes, p.ck, r, c[g]);
-                if (p.gate_rows) slots.copy(n + 2 * G, row_of<T>(p.gate, r / p.gate_rows), c[g]);
+                slots.template copy_row<kA>(n, p.x, p.x_codes, p.ck, r, c[g]);
+                if (p.has_branch)
+                    slots.template copy_row<kA>(n + G, p.h, p.h_codes, p.ck, r, c[g]);
+                if (p.gate_rows)
+                    slots.template copy<kA>(n + 2 * G, row_of<T>(p.gate, r / p.gate_rows), c[g]);
+            } else {
+                nx[g] = load_row<T, kA>(p.x, p.x_codes, p.ck, r, c[g]);
+                if (p.has_branch) nh[g] = load_row<T, kA>(p.h, p.h_codes, p.ck, r, c[g]);
+                if (p.gate_rows)
+                    ng[g] = load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c[g]);
             }
         }
     };
+    // vectors into their slots; columns that do not exist are zeros in every slot
+    const void* const vectors[S::kVectors] = {p.post_w, p.post_b, p.pre_w, p.pre_b};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        if (!c[g].whole())
+            for (uint32_t n = g; n < (S::kVectors + S::kDepth * S::kOps) * G; n += G) slots.clear(n);
+#pragma unroll
+        for (int n = 0; n < (int)S::kVectors; ++n)
+            if (vectors[n]) slots.put(n * G + g, load_raw<T, kA>((const T*)vectors[n], c[g]));
+    }
+    constexpr uint32_t kAhead = S::kPipe ? S::kDepth : 1;
     uint32_t r = cluster * teams + team, ahead = r, stage = 0;
-    if constexpr (kA == kWide) {
 #pragma unroll
-        for (uint32_t k = 0; k < S::kDepth; ++k) {
-            if (ahead < p.rows) fetch(ahead, k);
-            ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
-            copy_commit();
-        }
-        const void* const vectors[S::kVectors] = {p.post_w, p.post_b, p.pre_w, p.pre_b};
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (!c[g].any())
-                for (uint32_t n = g; n < (S::kVectors + S::kDepth * S::kOps) * G; n += G)
-                    slots.clear(n);
-#pragma unroll
-            for (int n = 0; n < (int)S::kVectors; ++n)
-                if (vectors[n]) slots.put(n * G + g, load_raw<T, kA>((const T*)vectors[n], c[g]));
-        }
+    for (uint32_t k = 0; k < kAhead; ++k) {
+        if (ahead < p.rows) fetch(ahead, k);
+        ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
+        if (S::kPipe) copy_commit();
     }
     for (; r < p.rows; r = stride < p.rows - r ? r + stride : p.rows) {
         Raw<T> rx[G], rh[G], rg[G];
-        if (kA == kWide) copy_wait<S::kDepth - 1>();
+        if (S::kPipe) copy_wait<kAhead - 1>();
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if constexpr (kA == kWide) {
+            if constexpr (S::kPipe) {
                 const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
-                rx[g] = slots.get_row(n, p.x_codes);
-                if (p.has_branch) rh[g] = slots.get_row(n + G, p.h_codes);
+                rx[g] = slots.template get_row<kA>(n, p.x, p.x_codes, p.ck, r, c[g]);
+                if (p.has_branch)
+                    rh[g] = slots.template get_row<kA>(n + G, p.h, p.h_codes, p.ck, r, c[g]);
                 if (p.gate_rows) rg[g] = slots.get(n + 2 * G);
             } else {
-                rx[g] = load_row<T, kA>(p.x, p.x_codes, p.ck, r, c[g]);
-                if (p.has_branch) rh[g] = load_row<T, kA>(p.h, p.h_codes, p.ck, r, c[g]);
-                if (p.gate_rows)
-                    rg[g] = load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c[g]);
+                rx[g] = nx[g];
+                rh[g] = nh[g];
+                rg[g] = ng[g];
             }
         }
-        if (kA == kWide) {   // the next row into the slots just read
-            if (ahead < p.rows) fetch(ahead, stage);
-            ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
+        if (ahead < p.rows) fetch(ahead, stage);   // the next row, into the slots just read
+        ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
+        if (S::kPipe) {
             copy_commit();
             stage = stage + 1 == S::kDepth ? 0 : stage + 1;
         }
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 4 ? 2 : 1
                 const float hr = centre<kA, G>(t, p.post, p.post_eps, inv_cols, c, h);
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    scale_shift<T, kA, G>(slots, g, c[g], hr, p.post_w, p.post_b, h[g]);
+                    scale_shift<T, G>(slots, g, hr, p.post_w, p.post_b, h[g]);
             }
             if (p.gate_rows) {
 #pragma unroll
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 4 ? 2 : 1
             const float yr = centre<kA, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                scale_shift<T, kA, G>(slots, 2 * G + g, c[g], yr, p.pre_w, p.pre_b, y[g]);
+                scale_shift<T, G>(slots, 2 * G + g, yr, p.pre_w, p.pre_b, y[g]);
                 store_raw<T, kA>(row_of<T>(p.u, r), c[g], narrow<T>(y[g]));
             }
         }
@@ -241,11 +239,10 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
     const uint32_t teams = ctas == 1 ? kForwardWarps / warps : 1;
     const unsigned threads = 32 * warps * teams;
     auto kernel = join_kernel<T, kA, G>;
-    const size_t smem = kA == kWide ? ForwardShape<T, G>::kThreadBytes * threads : 0;
+    const size_t smem = ForwardShape<T, kA, G>::kThreadBytes * threads;
     int per_sm = 1;
     const cudaError_t e = resident(kernel, di.dev, threads, smem,
-                                   kA == kWide ? ForwardShape<T, G>::kThreadBytes * 32 * kForwardWarps
-                                               : 0,
+                                   ForwardShape<T, kA, G>::kThreadBytes * 32 * kForwardWarps,
                                    &per_sm);
     if (e != cudaSuccess) return e;
     const uint64_t clusters = ((uint64_t)a.rows + teams - 1) / teams;

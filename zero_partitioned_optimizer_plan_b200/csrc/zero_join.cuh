@@ -135,11 +135,21 @@ struct Slots {
                          "r"(r.w[4 * k + 3])
                          : "memory");
     }
-    // a lane's columns of a row of a matrix, or the codes and scale of a checkpoint's
-    __device__ __forceinline__ void copy(uint32_t n, const T* row, const Cols<kWide>& c) const {
-        if (!c.any()) return;
+    // a lane's columns of a row of a matrix (kNarrow: 32-bit values), or the codes and scale of a
+    // checkpoint's (kWide)
+    template <int kA>
+    __device__ __forceinline__ void copy(uint32_t n, const T* row, const Cols<kA>& c) const {
+        if constexpr (kA == kWide) {
+            if (!c.any()) return;
 #pragma unroll
-        for (uint32_t k = 0; k < kWords; ++k) copy_async(word(n, k), row + c.c0 + k * 16 / sizeof(T), 16);
+            for (uint32_t k = 0; k < kWords; ++k)
+                copy_async(word(n, k), row + c.c0 + k * 16 / sizeof(T), 16);
+        } else {
+            static_assert(sizeof(T) == 4, "cp.async moves 4 bytes at least");
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c.mask >> j & 1u) copy_async(word(n, j / 4) + 4 * (j % 4), row + c.at(j), 4);
+        }
     }
     __device__ __forceinline__ void copy_codes(uint32_t n, const uint8_t* row, const CkptShape& s,
                                                const Cols<kWide>& c) const {
@@ -147,21 +157,32 @@ struct Slots {
         copy_async(word(n, 0), row + c.c0, 8);
         copy_async(word(n, 0) + 8, ckpt_scales(row, s) + (c.c0 >> 7), 4);
     }
+    // (kNarrow leaves a checkpoint's row to get_row: its single bytes cannot be copied)
+    template <int kA>
     __device__ __forceinline__ void copy_row(uint32_t n, const Rows& m, bool codes,
                                              const CkptShape& s, uint32_t r,
-                                             const Cols<kWide>& c) const {
-        if (codes)
+                                             const Cols<kA>& c) const {
+        if (!codes)
+            copy<kA>(n, row_of<T>(m, r), c);
+        else if constexpr (kA == kWide)
             copy_codes(n, row_of<uint8_t>(m, r), s, c);
-        else
-            copy(n, row_of<T>(m, r), c);
     }
-    // values of a slot that copy_row filled
-    __device__ __forceinline__ Raw<T> get_row(uint32_t n, bool codes) const {
-        Raw<T> r = get(n);
-        if (codes) r.w[3] = r.w[2];
-        return r;
+    // values of row r, from the slot that copy_row filled
+    template <int kA>
+    __device__ __forceinline__ Raw<T> get_row(uint32_t n, const Rows& m, bool codes,
+                                              const CkptShape& s, uint32_t r,
+                                              const Cols<kA>& c) const {
+        if (kA == kNarrow && codes) return load_codes<T, kA>(row_of<uint8_t>(m, r), s, c);
+        Raw<T> v = get(n);
+        if (codes) v.w[3] = v.w[2];
+        return v;
     }
 };
+
+// Whether rows travel through slots: 16-bit values that cannot move as 16 bytes go through
+// registers, one row ahead.
+template <typename T, int kA>
+constexpr bool piped() { return kA == kWide || sizeof(T) == 4; }
 
 // Let a kernel use up to `most` bytes of dynamic shared memory on device `dev`, and tell how many
 // of its CTAs (threads, smem) an SM holds at once. Asked once per host thread and shape.

@@ -68,7 +68,8 @@ struct BackShape {
     static constexpr int kWarps = sizeof(T) == 4 || kMany ? 8 : G == 2 ? 12 : 16;
     static constexpr uint32_t kOps = kHeavy ? 5 : 4;       // y, du, dy, gate, h
     static constexpr uint32_t kVectors = kHeavy ? 3 : 1;   // pre_w, post_w, post_b
-    static constexpr uint32_t kDepth = G == 2 && !kHeavy ? 3 : 4;   // rows on the way
+    static constexpr bool kPipe = piped<T, kA>();
+    static constexpr uint32_t kDepth = !kPipe ? 0 : G == 2 && !kHeavy ? 3 : 4;   // rows on the way
     static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
     static constexpr size_t kThreadBytes = (size_t)kSlots * 8 * sizeof(T);
     static constexpr size_t kBytes = kThreadBytes * 32 * kWarps +
@@ -149,50 +150,54 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
     grid_wait();
     if (g.ctas > 1) cluster_barrier();   // every CTA of the cluster is there before the first store
 
-    // kWide: rows and vectors in this thread's slots of shared memory. kNarrow: the next row's
-    // loads in registers.
+    // the vectors, and rows on their way, in this thread's slots of shared memory
     extern __shared__ uint4 dynamic[];
     const Slots<T> slots{smem_addr(dynamic) + threadIdx.x * 16u, blockDim.x};
     Raw<T> ry[G], rh[G], rdu[G], rdy[G];
     auto fetch = [&](uint32_t r, uint32_t stage) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            if constexpr (kA == kWide) {
+            if constexpr (S::kPipe) {
                 const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
                 if (has_du) {
-                    slots.copy_row(n, p.x, y_codes, p.ck, r, c[i]);
-                    slots.copy(n + G, row_of<T>(p.du, r), c[i]);
+                    slots.template copy_row<kA>(n, p.x, y_codes, p.ck, r, c[i]);
+                    slots.template copy<kA>(n + G, row_of<T>(p.du, r), c[i]);
                 }
-                if (p.dy.p) slots.copy(n + 2 * G, row_of<T>(p.dy, r), c[i]);
-                if (p.gate_rows) slots.copy(n + 3 * G, row_of<T>(p.gate, r / p.gate_rows), c[i]);
-                if (kPost || kGate) slots.copy_row(n + 4 * G, p.h, h_codes, p.ck, r, c[i]);
+                if (p.dy.p) slots.template copy<kA>(n + 2 * G, row_of<T>(p.dy, r), c[i]);
+                if (p.gate_rows)
+                    slots.template copy<kA>(n + 3 * G, row_of<T>(p.gate, r / p.gate_rows), c[i]);
+                if (kPost || kGate)
+                    slots.template copy_row<kA>(n + 4 * G, p.h, h_codes, p.ck, r, c[i]);
             } else {
                 if (has_du) {
                     ry[i] = load_row<T, kA>(p.x, y_codes, p.ck, r, c[i]);
                     rdu[i] = load_raw<T, kA>(row_of<T>(p.du, r), c[i]);
                 }
+                if (p.dy.p) rdy[i] = load_raw<T, kA>(row_of<T>(p.dy, r), c[i]);
                 if (kPost || kGate) rh[i] = load_row<T, kA>(p.h, h_codes, p.ck, r, c[i]);
             }
         }
     };
     auto vector = [&](int n, int i, const void* v, float none, F8& out) {
-        if (kA == kWide && v)
+        if (v) {
             widen<T>(slots.get(n * G + i), out);
-        else
-            load_vec<T, kA>(v, none, c[i], out);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[k] = both(none);
+        }
     };
-    if constexpr (kA == kWide) {
+    {
         const void* const vectors[3] = {p.pre_w, p.post_w, p.post_b};
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            if (!c[i].any())
+            if (!c[i].whole())
                 for (uint32_t n = i; n < S::kSlots; n += G) slots.clear(n);
 #pragma unroll
             for (int n = 0; n < (int)S::kVectors; ++n)
                 if (vectors[n]) slots.put(n * G + i, load_raw<T, kA>((const T*)vectors[n], c[i]));
         }
     }
-    constexpr uint32_t kLoads = kA == kWide ? S::kDepth : 1;   // rows ahead
+    constexpr uint32_t kLoads = S::kPipe ? S::kDepth : 1;   // rows ahead
     Walk in(cluster * g.teams + team), at = in;
     in.open(g, p.rows);
     at.open(g, p.rows);
@@ -202,36 +207,36 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
             fetch(in.row, k);
             in.next(g, p.rows);
         }
-        if (kA == kWide) copy_commit();
+        if (S::kPipe) copy_commit();
     }
     uint32_t stage = 0;
     while (at.row < at.end) {
         const uint32_t r = at.row, unit = at.unit;
         F8 y[G], h[G], du[G], gy[G], gate[G];
-        if (kA == kWide) copy_wait<kLoads - 1>();
+        if (S::kPipe) copy_wait<kLoads - 1>();
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            if constexpr (kA == kWide) {
+            if constexpr (S::kPipe) {
                 const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
                 if (has_du) {
-                    widen_row<T>(slots.get_row(n, y_codes), y_codes, y[i]);
+                    widen_row<T>(slots.template get_row<kA>(n, p.x, y_codes, p.ck, r, c[i]),
+                                 y_codes, y[i]);
                     widen<T>(slots.get(n + G), du[i]);
                 }
-                if (p.dy.p) {
-                    widen<T>(slots.get(n + 2 * G), gy[i]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) gy[i][k] = 0;
-                }
+                if (p.dy.p) widen<T>(slots.get(n + 2 * G), gy[i]);
                 if (p.gate_rows) widen<T>(slots.get(n + 3 * G), gate[i]);
-                if (kPost || kGate) widen_row<T>(slots.get_row(n + 4 * G, h_codes), h_codes, h[i]);
+                if (kPost || kGate)
+                    widen_row<T>(slots.template get_row<kA>(n + 4 * G, p.h, h_codes, p.ck, r, c[i]),
+                                 h_codes, h[i]);
             } else {
                 if (has_du) {
                     widen_row<T>(ry[i], y_codes, y[i]);
                     widen<T>(rdu[i], du[i]);
                 }
+                if (p.dy.p) widen<T>(rdy[i], gy[i]);
                 if (kPost || kGate) widen_row<T>(rh[i], h_codes, h[i]);
-                if (p.dy.p) rdy[i] = load_raw<T, kA>(row_of<T>(p.dy, r), c[i]);
+            }
+            if (!p.dy.p) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) gy[i][k] = 0;
             }
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
             fetch(in.row, stage);
             in.next(g, p.rows);
         }
-        if (kA == kWide) {
+        if (S::kPipe) {
             copy_commit();
             stage = stage + 1 == S::kDepth ? 0 : stage + 1;
         }
@@ -290,10 +295,6 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
             team_sum<4>(t, s);
             if (kPost)
                 hr = __frsqrt_rn(__fadd_rn(__fmul_rn(s[3], g.inv_cols), p.post_eps));
-            if (kA == kNarrow && p.dy.p) {
-#pragma unroll
-                for (int i = 0; i < G; ++i) widen<T>(rdy[i], gy[i]);
-            }
             if (has_du) {
                 const float yr = __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], g.inv_cols), p.pre_eps));
                 const float m1 = pre_layer ? __fmul_rn(s[1], g.inv_cols) : 0.0f;
@@ -311,9 +312,6 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
                     if (pre_layer) clear_missing<kA>(c[i], gy[i]);
                 }
             }
-        } else if (kA == kNarrow && p.dy.p) {
-#pragma unroll
-            for (int i = 0; i < G; ++i) widen<T>(rdy[i], gy[i]);
         }
         if (p.dx.p) {
 #pragma unroll
@@ -342,7 +340,7 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
                     }
                 }
                 if (p.gate_rows) {
-                    if (kA == kNarrow)
+                    if (!S::kPipe)
                         widen<T>(load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c[i]), gate[i]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) gy[i][k] = f2_mul(gy[i][k], gate[i][k]);
@@ -512,10 +510,10 @@ cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, Bac
     if (a.rows == 0) return cudaSuccess;
     auto kernel = join_back_kernel<T, kA, kPost, kGate, G>;
     const unsigned threads = 32 * g.warps * g.teams;
-    const size_t smem = kA == kWide ? S::kThreadBytes * threads : 0;
+    const size_t smem = S::kThreadBytes * threads;
     int ctas = 1;
-    const cudaError_t e = resident(kernel, di.dev, threads, smem,
-                                   kA == kWide ? S::kThreadBytes * 32 * S::kWarps : 0, &ctas);
+    const cudaError_t e = resident(kernel, di.dev, threads, smem, S::kThreadBytes * 32 * S::kWarps,
+                                   &ctas);
     if (e != cudaSuccess) return e;
     const bool used = g.clusters > 1 || (a.dgate.p && g.parts > 1);
     return launch_clusters(kernel, g.clusters, g.ctas, threads, smem, stream, a, g,

@@ -6,8 +6,10 @@
 //
 // A pair of CTAs (two SMs, tcgen05 cta_group::2) computes 256 x 256 outputs, 64 tokens per stage:
 //   A  dy^T, 128 features per CTA, by TMA with the 128-byte swizzle (zeros outside the matrix);
-//      a dy that TMA cannot address (base or stride not 16-byte aligned) is loaded by the same
-//      warps that make B, and stored into the same layout.
+//      a dy with an out-feature count that is no multiple of 8 is first copied to aligned rows in
+//      the workspace (its rows' starts differ in alignment; loading it in place by the warps that
+//      make B took 117 us where the copy and the product take a third); one whose count is, but
+//      whose base or stride is not 16-byte aligned, is loaded in place.
 //   B  a, 128 features (one block of codes) per CTA. TMA brings the codes and their scales, eight
 //      warps form T(q*scale) as zero_ckpt_load_q8 does and store the tile swizzled. (Codes loaded
 //      by those warps into registers, stages ahead, were 4 times slower: the fence between their
@@ -109,9 +111,13 @@ WgradPlan wgrad_plan(uint64_t t, uint64_t o, uint64_t i) {
 
 }  // namespace
 
-uint64_t wgrad_workspace(uint64_t t, uint64_t o, uint64_t i) {
-    const WgradPlan p = wgrad_plan(t, o, i);
+// Partial tiles, then the aligned copy of dy.
+static uint64_t partial_bytes(const WgradPlan& p) {
     return p.splits > 1 ? (uint64_t)p.tiles_o * p.tiles_i * p.splits * 256 * p.m * kTileI * 4 : 0;
+}
+
+uint64_t wgrad_workspace(uint64_t t, uint64_t o, uint64_t i) {
+    return partial_bytes(wgrad_plan(t, o, i)) + (o % 8 ? t * ((o + 7) / 8 * 8) * 2 : 0);
 }
 
 namespace {
@@ -646,6 +652,41 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(WgradArgs a, WgradPlan 
     }
 }
 
+// dy's rows to aligned rows of `pitch` (a multiple of 8) values; the values behind a row are not
+// read later. A thread moves eight values: five 4-byte loads shifted together where the source is
+// not 4-byte aligned (four where it is), single loads at a row's ends.
+__global__ void __launch_bounds__(256) align_rows_kernel(uint64_t rows, uint32_t cols, Mat src,
+                                                         uint16_t* dst, uint32_t pitch) {
+    grid_wait();
+    grid_launch_next();
+    const uint32_t chunks = pitch / 8;
+    const uint64_t total = rows * chunks;
+    for (uint64_t e = (uint64_t)blockIdx.x * 256 + threadIdx.x; e < total;
+         e += (uint64_t)gridDim.x * 256) {
+        const uint64_t r = e / chunks;
+        const uint32_t c = (uint32_t)(e - r * chunks) * 8;
+        const uint16_t* p = (const uint16_t*)src.p + r * src.ld + c;
+        uint32_t w[4];
+        if (c > 0 && c + 8 < cols) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>((uintptr_t)p & ~(uintptr_t)3);
+            const uint32_t shift = ((uintptr_t)p & 2u) * 8u;   // 0 or 16 bits
+            uint32_t v[5];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __ldg(q + j);
+            v[4] = shift ? __ldg(q + 4) : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], shift);
+        } else {
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? __ldg(p + j) : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = v[2 * j] | v[2 * j + 1] << 16;
+        }
+        *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -727,9 +768,18 @@ cudaError_t run_wgrad(const WgradArgs& a, int dtype, void* ws, cudaStream_t stre
     c.partial = c.plan.splits > 1 ? (float*)ws : nullptr;
     c.vec = aligned16(a.dw.p) && a.dw.ld % 8 == 0 ? 16 : 2;
     if (a.tokens) {
-        const bool tma = aligned16(a.dy.p) && a.dy.ld % 8 == 0;
+        bool tma = aligned16(a.dy.p) && a.dy.ld % 8 == 0;
+        if (!tma && a.outf % 8 != 0) {
+            const uint32_t pitch = (a.outf + 7) / 8 * 8;
+            uint16_t* copy = reinterpret_cast<uint16_t*>((char*)ws + partial_bytes(c.plan));
+            e = launch_act(align_rows_kernel, dim3(plain_grid(a.tokens * (pitch / 8), di.sms, 16)),
+                           256, 0, stream, a.tokens, a.outf, a.dy, copy, pitch);
+            if (e != cudaSuccess) return e;
+            c.a.dy = Mat{copy, pitch};
+            tma = true;
+        }
         WgradMaps maps = {};
-        e = make_maps(a, dtype, tma, &maps);
+        e = make_maps(c.a, dtype, tma, &maps);
         if (e != cudaSuccess) return e;
         e = c.plan.m == 2 ? (tma ? run_pairs<T, true, 2>(c, maps, di.sms, stream)
                                  : run_pairs<T, false, 2>(c, maps, di.sms, stream))
