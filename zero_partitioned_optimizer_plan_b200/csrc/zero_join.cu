@@ -74,7 +74,8 @@ __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint3
     }
 }
 
-constexpr int kForwardWarps = 8;   // of a CTA; rows that need more are shared by a cluster
+// A CTA has kW warps at most, 8 or (rows of more than 4096 columns) 16; still wider rows are
+// shared by the CTAs of a cluster.
 
 // Rows on the way: what lets two CTAs (three of one 16-bit chunk per lane) fit an SM.
 template <typename T, int kA, int G>
@@ -86,8 +87,8 @@ struct ForwardShape {
     static constexpr size_t kThreadBytes = (size_t)(kVectors + kDepth * kOps) * G * 8 * sizeof(T);
 };
 
-template <typename T, int kA, int G>
-__global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 4 ? 2 : 1)
+template <typename T, int kA, int G, int kW>
+__global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && kA == kWide ? 3 : 2)
     join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
     using S = ForwardShape<T, kA, G>;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
@@ -231,18 +232,18 @@ __global__ void __launch_bounds__(32 * kForwardWarps, sizeof(T) * G <= 4 ? 2 : 1
     if (ctas > 1) cluster_barrier();   // no CTA leaves while another may still store into it
 }
 
-template <typename T, int kA, int G>
+template <typename T, int kA, int G, int kW>
 cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t stream) {
     uint32_t warps = (chunks_of(a.cols) + G - 1) / G, ctas = 1;
-    while ((warps + ctas - 1) / ctas > (uint32_t)kForwardWarps) ctas *= 2;
+    while ((warps + ctas - 1) / ctas > (uint32_t)kW) ctas *= 2;
     warps = (warps + ctas - 1) / ctas;
-    const uint32_t teams = ctas == 1 ? kForwardWarps / warps : 1;
+    const uint32_t teams = ctas == 1 ? kW / warps : 1;
     const unsigned threads = 32 * warps * teams;
-    auto kernel = join_kernel<T, kA, G>;
+    auto kernel = join_kernel<T, kA, G, kW>;
     const size_t smem = ForwardShape<T, kA, G>::kThreadBytes * threads;
     int per_sm = 1;
     const cudaError_t e = resident(kernel, di.dev, threads, smem,
-                                   ForwardShape<T, kA, G>::kThreadBytes * 32 * kForwardWarps,
+                                   ForwardShape<T, kA, G>::kThreadBytes * 32 * kW,
                                    &per_sm);
     if (e != cudaSuccess) return e;
     const uint64_t clusters = ((uint64_t)a.rows + teams - 1) / teams;
@@ -252,17 +253,23 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
 }
 
 // Chunks per lane: two, so that the work per row that does not grow with the columns is shared by
-// more of them; one where a row has one chunk or three, or where there are too few rows to fill
-// the device anyway.
+// more of them (16384 x 2048 fp16 with both checkpoints: 123 us, with one 146); one where a row
+// has three or fewer, where it has 32-bit values (registers), or where there are too few rows to
+// fill the device anyway.
 template <typename T, int kA>
 cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
     DevInfo di;
     const cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
     const uint32_t chunks = chunks_of(a.cols);
-    if (chunks <= 1 || chunks == 3 || (chunks <= kForwardWarps && a.rows <= (uint32_t)di.sms))
-        return run_forward<T, kA, 1>(a, di, stream);
-    return run_forward<T, kA, 2>(a, di, stream);
+    if (chunks <= 3 || (chunks <= 8 && (sizeof(T) == 4 || a.rows <= (uint32_t)di.sms)))
+        return run_forward<T, kA, 1, 8>(a, di, stream);
+    if constexpr (sizeof(T) == 4) {
+        return run_forward<T, kA, 1, 16>(a, di, stream);
+    } else {
+        if (chunks <= 16) return run_forward<T, kA, 2, 8>(a, di, stream);
+        return run_forward<T, kA, 2, 16>(a, di, stream);
+    }
 }
 
 template <typename T>

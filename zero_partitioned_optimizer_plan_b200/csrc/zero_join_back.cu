@@ -59,17 +59,17 @@ BackGeom back_geom(uint32_t rows, uint64_t cols, uint32_t group_rows, uint32_t l
 
 // The shape of one instantiation. A lane holds G chunks (256 columns per warp) of each matrix and
 // the column sums of up to four vectors in registers: one 16-bit chunk takes 128 of them (16 warps
-// per SM), two take 168 without a norm after the block (12 warps) and else, as 32-bit ones do, up
-// to 255 (8 warps).
+// per SM), two without a norm after the block, or a 32-bit one, 168 (12 warps).
 template <typename T, int kA, bool kPost, bool kGate, int G>
 struct BackShape {
     static constexpr bool kHeavy = kPost || kGate;
-    static constexpr bool kMany = (G == 2 && kHeavy) || (kA == kNarrow && kPost && kGate);
-    static constexpr int kWarps = sizeof(T) == 4 || kMany ? 8 : G == 2 ? 12 : 16;
+    static constexpr int kWarps = kA == kNarrow && sizeof(T) == 2 && kPost && kGate ? 8
+                                  : sizeof(T) == 4 || G == 2                      ? 12
+                                                                                  : 16;
     static constexpr uint32_t kOps = kHeavy ? 5 : 4;       // y, du, dy, gate, h
     static constexpr uint32_t kVectors = kHeavy ? 3 : 1;   // pre_w, post_w, post_b
     static constexpr bool kPipe = piped<T, kA>();
-    static constexpr uint32_t kDepth = !kPipe ? 0 : G == 2 && !kHeavy ? 3 : 4;   // rows on the way
+    static constexpr uint32_t kDepth = !kPipe ? 0 : sizeof(T) == 4 ? 2 : G == 2 ? 3 : 4;   // rows on the way
     static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
     static constexpr size_t kThreadBytes = (size_t)kSlots * 8 * sizeof(T);
     static constexpr size_t kBytes = kThreadBytes * 32 * kWarps +
@@ -493,13 +493,6 @@ __global__ void __launch_bounds__(32 * kSumRows)
         put_sum<T>(row_of<T>(p.dgate, k - 4), c, v, p.accumulate & ZERO_ACC_GATE);
 }
 
-// Two chunks per lane of 16-bit rows wider than one (what a row costs beside its columns is then
-// paid by half the warps): 16384 x 2048 fp16 without a norm after the block, 112 us with one.
-template <typename T>
-int lane_chunks(const JoinArgs& a, Access access) {
-    return sizeof(T) == 2 && access == kWide && chunks_of(a.cols) > 1 ? 2 : 1;
-}
-
 template <typename T, int kA, bool kPost, bool kGate, int G>
 cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, BackGeom* geom,
                             cudaStream_t stream) {
@@ -520,15 +513,23 @@ cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, Bac
                            used ? ws : (float*)nullptr);
 }
 
-template <typename T, int kA, int G>
+// Two chunks per lane for 16-bit rows wider than one in a boundary without a norm after the block
+// and a gate (16384 x 2048 fp16: 107 us, with one 112); with them the registers leave so few warps
+// that one is faster (8192 x 4096 bf16: 187 us, with two 198). The choice does not go by the
+// outputs asked for: dx and dh have the same bits with and without the others.
+template <typename T, int kA>
 cudaError_t run_back_any(const JoinArgs& a, const DevInfo& di, float* ws, BackGeom* g,
                          cudaStream_t stream) {
     const bool post = a.post != ZERO_NORM_NONE && (a.dh.p || a.dgate.p || a.dpost_w || a.dpost_b);
     if (post)
-        return a.dgate.p ? run_back_kernel<T, kA, true, true, G>(a, di, ws, g, stream)
-                         : run_back_kernel<T, kA, true, false, G>(a, di, ws, g, stream);
-    return a.dgate.p ? run_back_kernel<T, kA, false, true, G>(a, di, ws, g, stream)
-                     : run_back_kernel<T, kA, false, false, G>(a, di, ws, g, stream);
+        return a.dgate.p ? run_back_kernel<T, kA, true, true, 1>(a, di, ws, g, stream)
+                         : run_back_kernel<T, kA, true, false, 1>(a, di, ws, g, stream);
+    if (a.dgate.p) return run_back_kernel<T, kA, false, true, 1>(a, di, ws, g, stream);
+    if constexpr (sizeof(T) == 2 && kA == kWide) {
+        if (chunks_of(a.cols) > 1 && a.post == ZERO_NORM_NONE && !a.gate.p)
+            return run_back_kernel<T, kA, false, false, 2>(a, di, ws, g, stream);
+    }
+    return run_back_kernel<T, kA, false, false, 1>(a, di, ws, g, stream);
 }
 
 template <typename T>
@@ -536,18 +537,9 @@ cudaError_t run_join_back(const JoinArgs& a, float* ws, cudaStream_t stream) {
     DevInfo di;
     cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
-    const Access access = all_access<T>(a);
     BackGeom g = {};
-    if constexpr (sizeof(T) == 2) {
-        if (lane_chunks<T>(a, access) == 2)
-            e = run_back_any<T, kWide, 2>(a, di, ws, &g, stream);
-        else
-            e = access == kWide ? run_back_any<T, kWide, 1>(a, di, ws, &g, stream)
-                                : run_back_any<T, kNarrow, 1>(a, di, ws, &g, stream);
-    } else {
-        e = access == kWide ? run_back_any<T, kWide, 1>(a, di, ws, &g, stream)
-                            : run_back_any<T, kNarrow, 1>(a, di, ws, &g, stream);
-    }
+    e = all_access<T>(a) == kWide ? run_back_any<T, kWide>(a, di, ws, &g, stream)
+                                  : run_back_any<T, kNarrow>(a, di, ws, &g, stream);
     if (e != cudaSuccess) return e;
     const bool vectors = (a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b) &&
                          (g.clusters > 1 || a.rows == 0);
