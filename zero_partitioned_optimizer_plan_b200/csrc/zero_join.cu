@@ -40,20 +40,27 @@ __device__ __forceinline__ float centre(Team& t, int kind, float eps, float inv_
     return __frsqrt_rn(__fadd_rn(__fmul_rn(s[0], inv_cols), eps));
 }
 
-// z*r*w + b; slots n and n + G hold w and b.
-template <typename T, int G>
-__device__ __forceinline__ void scale_shift(const Slots<T>& slots, uint32_t n, float r, bool w,
-                                            bool b, F8& z) {
+// z*r*w + b; slots n and n + G hold w and b, where there is room (see ForwardShape).
+template <typename T, int kA, int G>
+__device__ __forceinline__ void scale_shift(const Slots<T>& slots, uint32_t n, const Cols<kA>& c,
+                                            float r, const void* w, const void* b, F8& z) {
+    constexpr bool kSlots = sizeof(T) * G <= 4;
     F8 wv;
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], both(r));
     if (w) {
-        widen<T>(slots.get(n), wv);
+        if (kSlots)
+            widen<T>(slots.get(n), wv);
+        else
+            load_vec<T, kA>(w, 1.0f, c, wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_mul(z[k], wv[k]);
     }
     if (b) {
-        widen<T>(slots.get(n + G), wv);
+        if (kSlots)
+            widen<T>(slots.get(n + G), wv);
+        else
+            load_vec<T, kA>(b, 0.0f, c, wv);
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = f2_add(z[k], wv[k]);
     }
@@ -80,7 +87,8 @@ __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint3
 // Rows on the way: what lets two CTAs (three of one 16-bit chunk per lane) fit an SM.
 template <typename T, int kA, int G>
 struct ForwardShape {
-    static constexpr uint32_t kVectors = 4;   // post_w, post_b, pre_w, pre_b
+    // post_w, post_b, pre_w, pre_b; two 32-bit chunks leave no room for them
+    static constexpr uint32_t kVectors = sizeof(T) * G <= 4 ? 4 : 0;
     static constexpr uint32_t kOps = 3;       // x, h, gate
     static constexpr bool kPipe = piped<T, kA>();
     static constexpr uint32_t kDepth = !kPipe ? 0 : sizeof(T) * G == 2 ? 4 : sizeof(T) * G == 4 ? 3 : 2;
@@ -127,7 +135,7 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
         }
     };
     // vectors into their slots; columns that do not exist are zeros in every slot
-    const void* const vectors[S::kVectors] = {p.post_w, p.post_b, p.pre_w, p.pre_b};
+    const void* const vectors[4] = {p.post_w, p.post_b, p.pre_w, p.pre_b};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         if (!c[g].whole())
@@ -181,7 +189,7 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
                 const float hr = centre<kA, G>(t, p.post, p.post_eps, inv_cols, c, h);
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    scale_shift<T, G>(slots, g, hr, p.post_w, p.post_b, h[g]);
+                    scale_shift<T, kA, G>(slots, g, c[g], hr, p.post_w, p.post_b, h[g]);
             }
             if (p.gate_rows) {
 #pragma unroll
@@ -224,7 +232,7 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
             const float yr = centre<kA, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                scale_shift<T, G>(slots, 2 * G + g, yr, p.pre_w, p.pre_b, y[g]);
+                scale_shift<T, kA, G>(slots, 2 * G + g, c[g], yr, p.pre_w, p.pre_b, y[g]);
                 store_raw<T, kA>(row_of<T>(p.u, r), c[g], narrow<T>(y[g]));
             }
         }
@@ -254,7 +262,8 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
 
 // Chunks per lane: two, so that the work per row that does not grow with the columns is shared by
 // more of them (16384 x 2048 fp16 with both checkpoints: 123 us, with one 146); one where a row
-// has three or fewer, where it has 32-bit values (registers), or where there are too few rows to
+// has three or fewer, where it has 32-bit values that move
+// singly, or where there are too few rows to
 // fill the device anyway.
 template <typename T, int kA>
 cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
@@ -262,9 +271,10 @@ cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
     const cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
     const uint32_t chunks = chunks_of(a.cols);
-    if (chunks <= 3 || (chunks <= 8 && (sizeof(T) == 4 || a.rows <= (uint32_t)di.sms)))
+    constexpr bool kOne = sizeof(T) == 4 && kA == kNarrow;
+    if (chunks <= 3 || (chunks <= 8 && (kOne || a.rows <= (uint32_t)di.sms)))
         return run_forward<T, kA, 1, 8>(a, di, stream);
-    if constexpr (sizeof(T) == 4) {
+    if constexpr (kOne) {
         return run_forward<T, kA, 1, 16>(a, di, stream);
     } else {
         if (chunks <= 16) return run_forward<T, kA, 2, 8>(a, di, stream);

@@ -83,8 +83,13 @@ __device__ __forceinline__ uint64_t both(float a) { return f2_pack(a, a); }
 // shared memory that only it reads (cp.async: no register holds a load in flight, and nothing
 // else the thread loads waits for them), kDepth rows ahead.
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes) {
-    if (bytes == 16)
+// Copies of 16 bytes bypass L1, unless the neighbouring half of a 32-byte sector is another copy
+// of the same warp's (32-bit values: through L1 it is fetched once).
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes,
+                                           bool halves = false) {
+    if (bytes == 16 && halves)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else if (bytes == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else if (bytes == 8)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -143,7 +148,7 @@ struct Slots {
             if (!c.any()) return;
 #pragma unroll
             for (uint32_t k = 0; k < kWords; ++k)
-                copy_async(word(n, k), row + c.c0 + k * 16 / sizeof(T), 16);
+                copy_async(word(n, k), row + c.c0 + k * 16 / sizeof(T), 16, kWords > 1);
         } else {
             static_assert(sizeof(T) == 4, "cp.async moves 4 bytes at least");
 #pragma unroll
