@@ -379,38 +379,56 @@ __device__ __forceinline__ void store_dy(const WgradArgs& a, uint32_t tile, uint
     }
 }
 
-// N consecutive values of dw's row to memory; `vec` bytes per store at most.
+// 32 consecutive values of a row of dw, 16-byte aligned.
 template <typename T>
-__device__ __forceinline__ void store_row(T* p, const uint32_t (&v)[32], uint32_t n, int vec,
-                                          bool add) {
-    if (n >= 32 && vec == 16) {
+__device__ __forceinline__ void store_row(T* p, const uint32_t (&v)[32], bool add) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float f[8];
+    for (int j = 0; j < 4; ++j) {
+        float f[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[8 * j + k]);
-            if (add) {
-                const uint4 o = *reinterpret_cast<const uint4*>(p + 8 * j);
-                const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[8 * j + k]);
+        if (add) {
+            const uint4 o = *reinterpret_cast<const uint4*>(p + 8 * j);
+            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint16_t h = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-                    T t;
-                    memcpy(&t, &h, 2);
-                    f[k] = __fadd_rn(to_f(t), f[k]);
-                }
+            for (int k = 0; k < 8; ++k) {
+                const uint16_t h = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+                T t;
+                memcpy(&t, &h, 2);
+                f[k] = __fadd_rn(to_f(t), f[k]);
             }
-            *reinterpret_cast<uint4*>(p + 8 * j) =
-                make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
-                           pack2<T>(f[6], f[7]));
         }
-        return;
+        *reinterpret_cast<uint4*>(p + 8 * j) = make_uint4(
+            pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
     }
+}
+
+// 32 rows (one per lane) x 32 columns of dw at any alignment: transposed between the lanes first,
+// so that a store covers 32 neighbours of one row (lane by lane along its own row, the 2-byte
+// stores took 77 us for 7085 x 668 outputs of 4 tokens, which now take 19).
+template <typename T>
+__device__ __forceinline__ void store_tile(T* p, uint64_t ld, uint32_t lane, uint32_t rows,
+                                           uint32_t cols, uint32_t (&v)[32], bool add) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < n) {
-            const float f = __uint_as_float(v[j]);
-            p[j] = from_f<T>(add ? __fadd_rn(to_f(p[j]), f) : f);
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!(i & s)) {
+                const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + s], s);
+                if (up)
+                    v[i] = x;
+                else
+                    v[i + s] = x;
+            }
+    }
+    if (lane >= cols) return;
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+        if (r < rows) {
+            T* q = p + r * ld + lane;
+            const float f = __uint_as_float(v[r]);
+            *q = from_f<T>(add ? __fadd_rn(to_f(*q), f) : f);
         }
 }
 
@@ -569,8 +587,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
             for (uint32_t c = first; c < first + kM * kTileI / 2; c += 32) {
-                const uint32_t row = c / kTileI * 256u + rank * kHalf + 32u * quarter + lane;
-                const uint32_t o = u.o0 + row, i = u.i0 + c % kTileI;
+                const uint32_t row0 = c / kTileI * 256u + rank * kHalf + 32u * quarter;
+                const uint32_t row = row0 + lane, o = u.o0 + row0, i = u.i0 + c % kTileI;
                 uint32_t v[32];
                 tmem_load(tmem + b * kTileI + c + (quarter << 21), v);
                 if (p.partial) {
@@ -582,8 +600,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                                              __uint_as_float(v[4 * j + 2]),
                                              __uint_as_float(v[4 * j + 3]));
                 } else if (o < p.a.outf && i < p.a.inf) {
-                    store_row<T>((T*)p.a.dw.p + o * p.a.dw.ld + i, v, p.a.inf - i, p.vec,
-                                 p.a.accumulate != 0);
+                    T* dw = (T*)p.a.dw.p + o * p.a.dw.ld + i;
+                    const uint32_t cols = p.a.inf - i, rows = p.a.outf - o;
+                    if (p.vec == 16 && cols >= 32) {
+                        if (lane < rows)
+                            store_row<T>(dw + lane * p.a.dw.ld, v, p.a.accumulate != 0);
+                    } else {
+                        store_tile<T>(dw, p.a.dw.ld, lane, rows, cols, v, p.a.accumulate != 0);
+                    }
                 }
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
