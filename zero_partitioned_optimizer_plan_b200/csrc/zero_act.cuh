@@ -141,7 +141,9 @@ __device__ __forceinline__ const float* ckpt_scales(const uint8_t* row, const Ck
 // Eight columns per lane. A warp covers 256 columns (two blocks of codes) of a row. With 16-byte
 // aligned rows a lane's columns are neighbours and move as 16-byte accesses (kWide: a row ends on
 // a lane's last column; kTail: it may end inside a lane's columns). Otherwise (kNarrow) lane l
-// takes columns l, l + 32, ..., so that a warp's narrow accesses still touch whole sectors.
+// takes the pairs of columns 2l + 64p, p = 0 .. 3, so that a warp's 4-byte accesses are neighbours;
+// 16-bit rows that start inside a 4-byte word are read and written by the words they overlap, the
+// halves exchanged between the lanes.
 // ---------------------------------------------------------------------------------------------
 constexpr uint32_t kWarpCols = 256;
 
@@ -153,13 +155,17 @@ struct Cols {
     uint32_t mask;   // bit j: column j exists
     __device__ __forceinline__ Cols() : c0(0), cols(0), mask(0) {}
     __device__ __forceinline__ Cols(uint32_t chunk, uint32_t lane, uint32_t n) : cols(n), mask(0) {
-        c0 = chunk * kWarpCols + (kA == kNarrow ? lane : 8u * lane);
+        c0 = chunk * kWarpCols + (kA == kNarrow ? 2u : 8u) * lane;
         const uint32_t left = n > c0 ? n - c0 : 0u;
-        const uint32_t count = kA == kNarrow ? (left + 31u) / 32u : left;
-        mask = count >= 8u ? 0xffu : (1u << count) - 1u;
+        if (kA == kNarrow) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mask |= (left > at(j) - c0 ? 1u : 0u) << j;
+        } else {
+            mask = left >= 8u ? 0xffu : (1u << left) - 1u;
+        }
     }
     __device__ __forceinline__ uint32_t at(int j) const {
-        return c0 + (kA == kNarrow ? 32 * j : j);
+        return c0 + (kA == kNarrow ? 64 * (j >> 1) + (j & 1) : j);
     }
     __device__ __forceinline__ bool any() const { return mask != 0; }
     // every column of the lane exists (kWide: or none does)
@@ -191,6 +197,19 @@ __device__ __forceinline__ Raw<T> load_raw(const T* row, const Cols<kA>& c) {
         return r;
     }
     if (kA == kWide || !c.any()) return r;
+    if constexpr (kA == kNarrow && sizeof(T) == 2) {
+        if ((reinterpret_cast<uintptr_t>(row) & 3u) == 0) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint16_t* q = reinterpret_cast<const uint16_t*>(row) + c.at(2 * p);
+                if (c.mask >> (2 * p + 1) & 1u)
+                    r.w[p] = *reinterpret_cast<const uint32_t*>(q);
+                else if (c.mask >> (2 * p) & 1u)
+                    r.w[p] = *q;
+            }
+            return r;
+        }
+    }
     // every load is issued (a missing column reads the lane's first one), then sorted out: the
     // loads do not wait for one another
     uint32_t v[8];
@@ -227,15 +246,17 @@ __device__ __forceinline__ Raw<T> load_codes(const uint8_t* row, const CkptShape
         r.w[1] = q.y;
         r.w[2] = r.w[3] = __float_as_uint(sc[c.c0 >> 7]);
     } else {
-        uint32_t v[8];
+        // (the second of a pair may be a byte of the padding: q = 0)
+        uint32_t v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = row[c.mask >> j & 1u ? c.at(j) : c.c0];
+        for (int p = 0; p < 4; ++p)
+            v[p] = c.mask >> (2 * p) & 1u
+                       ? *reinterpret_cast<const uint16_t*>(row + c.at(2 * p))
+                       : 0x8080u;
+        r.w[0] = v[0] | v[1] << 16;
+        r.w[1] = v[2] | v[3] << 16;
         r.w[2] = __float_as_uint(sc[c.c0 >> 7]);
         r.w[3] = __float_as_uint(sc[(c.c0 >> 7) + (c.mask >> 4 & 1u)]);
-        r.w[0] = r.w[1] = 0u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            r.w[j / 4] |= (c.mask >> j & 1u ? v[j] : 128u) << 8 * (j & 3);
     }
     return r;
 }
@@ -351,6 +372,41 @@ __device__ __forceinline__ Raw<T> narrow(const F8& v) {
     return r;
 }
 
+// A lane's four pairs of 16-bit values to a row; every lane of the warp calls it. In a row that
+// starts inside a 4-byte word a pair (c, c + 1) straddles two of them: the lane stores the word
+// of c - 1 (from the lane before, or its own pair before across the wrap) and c, and single
+// values only at the two ends of the warp's columns and of the row.
+__device__ __forceinline__ void store_pairs(uint16_t* row, const Cols<kNarrow>& c,
+                                            const uint32_t (&w)[4]) {
+    if ((reinterpret_cast<uintptr_t>(row) & 3u) == 0) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint16_t* q = row + c.at(2 * p);
+            if (c.mask >> (2 * p + 1) & 1u)
+                *reinterpret_cast<uint32_t*>(q) = w[p];
+            else if (c.mask >> (2 * p) & 1u)
+                *q = (uint16_t)w[p];
+        }
+        return;
+    }
+    const uint32_t lane = threadIdx.x & 31u;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t give = lane == 31u ? (p > 0 ? w[p > 0 ? p - 1 : 0] : 0u) : w[p];
+        const uint32_t before = __shfl_sync(0xffffffffu, give, (lane + 31u) & 31u);
+        const uint32_t col = c.at(2 * p);
+        const bool own = c.mask >> (2 * p) & 1u;
+        if (p == 0 && lane == 0) {
+            if (own) row[col] = (uint16_t)w[p];
+        } else if (own) {
+            *reinterpret_cast<uint32_t*>(row + col - 1) = before >> 16 | w[p] << 16;
+        } else if (col == c.cols) {
+            row[col - 1] = (uint16_t)(before >> 16);
+        }
+        if (p == 3 && lane == 31u && (c.mask >> 7 & 1u)) row[col + 1] = (uint16_t)(w[p] >> 16);
+    }
+}
+
 template <typename T, int kA>
 __device__ __forceinline__ void store_raw(T* row, const Cols<kA>& c, const Raw<T>& r) {
     if (kA != kNarrow && c.whole()) {
@@ -361,13 +417,17 @@ __device__ __forceinline__ void store_raw(T* row, const Cols<kA>& c, const Raw<T
         return;
     }
     if (kA == kWide) return;
+    if constexpr (kA == kNarrow && sizeof(T) == 2) {
+        store_pairs(reinterpret_cast<uint16_t*>(row), c, r.w);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (!(c.mask >> j & 1u)) continue;
-        if constexpr (sizeof(T) == 4)
-            reinterpret_cast<uint32_t*>(row)[c.at(j)] = r.w[j];
-        else
-            reinterpret_cast<uint16_t*>(row)[c.at(j)] = (uint16_t)(r.w[j / 2] >> 16 * (j & 1));
+        for (int j = 0; j < 8; ++j) {
+            if (!(c.mask >> j & 1u)) continue;
+            if constexpr (sizeof(T) == 4)
+                reinterpret_cast<uint32_t*>(row)[c.at(j)] = r.w[j];
+            else
+                reinterpret_cast<uint16_t*>(row)[c.at(j)] = (uint16_t)(r.w[j / 2] >> 16 * (j & 1));
+        }
     }
 }
 
@@ -470,9 +530,10 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const CkptShape& s, co
             *reinterpret_cast<float*>(row + s.code_bytes + 4u * block) = scale[0];
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c.at(j) < s.code_bytes)
-                row[c.at(j)] = (uint8_t)((j < 4 ? w.x : w.y) >> 8 * (j & 3));
+        for (int p = 0; p < 4; ++p)
+            if (c.at(2 * p) < s.code_bytes)
+                *reinterpret_cast<uint16_t*>(row + c.at(2 * p)) =
+                    (uint16_t)((p < 2 ? w.x : w.y) >> 16 * (p & 1));
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (lane == 0 && block + k < s.blocks)

@@ -90,9 +90,8 @@ struct ForwardShape {
     // post_w, post_b, pre_w, pre_b; two 32-bit chunks leave no room for them
     static constexpr uint32_t kVectors = sizeof(T) * G <= 4 ? 4 : 0;
     static constexpr uint32_t kOps = 3;       // x, h, gate
-    static constexpr bool kPipe = piped<T, kA>();
-    static constexpr uint32_t kDepth = !kPipe ? 0 : sizeof(T) * G == 2 ? 4 : sizeof(T) * G == 4 ? 3 : 2;
-    static constexpr size_t kThreadBytes = (size_t)(kVectors + kDepth * kOps) * G * 8 * sizeof(T);
+    static constexpr uint32_t kDepth = sizeof(T) * G == 2 ? 4 : sizeof(T) * G == 4 ? 3 : 2;
+    static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
 };
 
 template <typename T, int kA, int G, int kW>
@@ -114,24 +113,15 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
     if (ctas > 1) cluster_barrier();   // every CTA is there before the first remote store
 
     extern __shared__ uint4 dynamic[];
-    const Slots<T> slots{smem_addr(dynamic) + threadIdx.x * 16u, blockDim.x};
-    Raw<T> nx[G], nh[G], ng[G];   // the next row's values, where they do not go through slots
+    const Slots<T> slots(smem_addr(dynamic), S::kSlots);
     auto fetch = [&](uint32_t r, uint32_t stage) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if constexpr (S::kPipe) {
-                const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
-                slots.template copy_row<kA>(n, p.x, p.x_codes, p.ck, r, c[g]);
-                if (p.has_branch)
-                    slots.template copy_row<kA>(n + G, p.h, p.h_codes, p.ck, r, c[g]);
-                if (p.gate_rows)
-                    slots.template copy<kA>(n + 2 * G, row_of<T>(p.gate, r / p.gate_rows), c[g]);
-            } else {
-                nx[g] = load_row<T, kA>(p.x, p.x_codes, p.ck, r, c[g]);
-                if (p.has_branch) nh[g] = load_row<T, kA>(p.h, p.h_codes, p.ck, r, c[g]);
-                if (p.gate_rows)
-                    ng[g] = load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c[g]);
-            }
+            const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
+            slots.template copy_row<kA>(n, p.x, p.x_codes, p.ck, r, c[g]);
+            if (p.has_branch) slots.template copy_row<kA>(n + G, p.h, p.h_codes, p.ck, r, c[g]);
+            if (p.gate_rows)
+                slots.template copy<kA>(n + 2 * G, row_of<T>(p.gate, r / p.gate_rows), c[g]);
         }
     };
     // vectors into their slots; columns that do not exist are zeros in every slot
@@ -139,42 +129,33 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         if (!c[g].whole())
-            for (uint32_t n = g; n < (S::kVectors + S::kDepth * S::kOps) * G; n += G) slots.clear(n);
+            for (uint32_t n = g; n < S::kSlots; n += G) slots.clear(n);
 #pragma unroll
         for (int n = 0; n < (int)S::kVectors; ++n)
             if (vectors[n]) slots.put(n * G + g, load_raw<T, kA>((const T*)vectors[n], c[g]));
     }
-    constexpr uint32_t kAhead = S::kPipe ? S::kDepth : 1;
     uint32_t r = cluster * teams + team, ahead = r, stage = 0;
 #pragma unroll
-    for (uint32_t k = 0; k < kAhead; ++k) {
+    for (uint32_t k = 0; k < S::kDepth; ++k) {
         if (ahead < p.rows) fetch(ahead, k);
         ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
-        if (S::kPipe) copy_commit();
+        copy_commit();
     }
     for (; r < p.rows; r = stride < p.rows - r ? r + stride : p.rows) {
         Raw<T> rx[G], rh[G], rg[G];
-        if (S::kPipe) copy_wait<kAhead - 1>();
+        copy_wait<S::kDepth - 1>();
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if constexpr (S::kPipe) {
-                const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
-                rx[g] = slots.template get_row<kA>(n, p.x, p.x_codes, p.ck, r, c[g]);
-                if (p.has_branch)
-                    rh[g] = slots.template get_row<kA>(n + G, p.h, p.h_codes, p.ck, r, c[g]);
-                if (p.gate_rows) rg[g] = slots.get(n + 2 * G);
-            } else {
-                rx[g] = nx[g];
-                rh[g] = nh[g];
-                rg[g] = ng[g];
-            }
+            const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
+            rx[g] = slots.template get_row<kA>(n, p.x, p.x_codes, r, c[g]);
+            if (p.has_branch) rh[g] = slots.template get_row<kA>(n + G, p.h, p.h_codes, r, c[g]);
+            if (p.gate_rows)
+                rg[g] = slots.template get<kA>(n + 2 * G, p.gate, r / p.gate_rows, c[g]);
         }
         if (ahead < p.rows) fetch(ahead, stage);   // the next row, into the slots just read
         ahead = stride < p.rows - min(ahead, p.rows) ? ahead + stride : p.rows;
-        if (S::kPipe) {
-            copy_commit();
-            stage = stage + 1 == S::kDepth ? 0 : stage + 1;
-        }
+        copy_commit();
+        stage = stage + 1 == S::kDepth ? 0 : stage + 1;
         if (p.save_h.p) {
             uint8_t* row = row_of<uint8_t>(p.save_h, r);
             save_all<T, kA, G>(row, p.ck, first, step, t.lane, rh);
@@ -248,10 +229,11 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
     const uint32_t teams = ctas == 1 ? kW / warps : 1;
     const unsigned threads = 32 * warps * teams;
     auto kernel = join_kernel<T, kA, G, kW>;
-    const size_t smem = ForwardShape<T, kA, G>::kThreadBytes * threads;
+    constexpr uint32_t kSlots = ForwardShape<T, kA, G>::kSlots;
+    const size_t smem = Slots<T>::bytes(kSlots, threads);
     int per_sm = 1;
     const cudaError_t e = resident(kernel, di.dev, threads, smem,
-                                   ForwardShape<T, kA, G>::kThreadBytes * 32 * kW,
+                                   Slots<T>::bytes(kSlots, 32 * kW),
                                    &per_sm);
     if (e != cudaSuccess) return e;
     const uint64_t clusters = ((uint64_t)a.rows + teams - 1) / teams;

@@ -108,9 +108,18 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // Slot n of this thread: 8 * sizeof(T) bytes as 16-byte words `threads` apart (no bank conflicts).
+// kNarrow 16-bit rows use one more 4-byte word per warp and slot, lane 0's, at `extra`.
 template <typename T>
 struct Slots {
     uint32_t base, threads;   // this thread's first word; threads of the CTA
+    uint32_t extra;           // this warp's first extra word; the next slot's is threads/8 away
+    __device__ __forceinline__ Slots(uint32_t smem, uint32_t count)
+        : base(smem + threadIdx.x * 16u), threads(blockDim.x),
+          extra(smem + count * kWords * blockDim.x * 16u + (threadIdx.x >> 5) * 4u) {}
+    // bytes of shared memory of `count` slots
+    static size_t bytes(uint32_t count, unsigned threads) {
+        return (size_t)count * (kWords * threads * 16u + threads / 8);
+    }
     static constexpr uint32_t kWords = sizeof(T) / 2;
     __device__ __forceinline__ uint32_t word(uint32_t n, uint32_t k) const {
         return base + (n * kWords + k) * threads * 16u;
@@ -140,8 +149,7 @@ struct Slots {
                          "r"(r.w[4 * k + 3])
                          : "memory");
     }
-    // a lane's columns of a row of a matrix (kNarrow: 32-bit values), or the codes and scale of a
-    // checkpoint's (kWide)
+    // a lane's columns of a row of a matrix
     template <int kA>
     __device__ __forceinline__ void copy(uint32_t n, const T* row, const Cols<kA>& c) const {
         if constexpr (kA == kWide) {
@@ -149,45 +157,107 @@ struct Slots {
 #pragma unroll
             for (uint32_t k = 0; k < kWords; ++k)
                 copy_async(word(n, k), row + c.c0 + k * 16 / sizeof(T), 16, kWords > 1);
-        } else {
-            static_assert(sizeof(T) == 4, "cp.async moves 4 bytes at least");
+        } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (c.mask >> j & 1u) copy_async(word(n, j / 4) + 4 * (j % 4), row + c.at(j), 4);
+        } else {
+            // the words that hold the pairs, or, where the row starts inside a word, those of
+            // each pair's first value and the one before it; lane 0 also the word behind the
+            // warp's columns. (A word at a row's end may hold two bytes of its neighbour.)
+            const uint32_t inside = (uint32_t)reinterpret_cast<uintptr_t>(row) & 2u;
+            const char* p = reinterpret_cast<const char*>(row) - inside;
+            const uint32_t last = c.cols + (inside ? 1u : 0u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c.at(2 * k) < last) copy_async(word(n, 0) + 4 * k, p + 2 * c.at(2 * k), 4);
+            if ((threadIdx.x & 31u) == 0 && c.c0 + kWarpCols < last)
+                copy_async(extra + n * (threads / 8), p + 2 * (c.c0 + kWarpCols), 4);
         }
     }
-    __device__ __forceinline__ void copy_codes(uint32_t n, const uint8_t* row, const CkptShape& s,
-                                               const Cols<kWide>& c) const {
-        if (!c.any()) return;
-        copy_async(word(n, 0), row + c.c0, 8);
-        copy_async(word(n, 0) + 8, ckpt_scales(row, s) + (c.c0 >> 7), 4);
-    }
-    // (kNarrow leaves a checkpoint's row to get_row: its single bytes cannot be copied)
+    // the same of a matrix or of a checkpoint: codes and scales (kNarrow: the warp's 256 codes as
+    // words l and l + 32, to be exchanged by get_row)
     template <int kA>
     __device__ __forceinline__ void copy_row(uint32_t n, const Rows& m, bool codes,
                                              const CkptShape& s, uint32_t r,
                                              const Cols<kA>& c) const {
-        if (!codes)
+        if (!codes) {
             copy<kA>(n, row_of<T>(m, r), c);
-        else if constexpr (kA == kWide)
-            copy_codes(n, row_of<uint8_t>(m, r), s, c);
+            return;
+        }
+        const uint8_t* row = row_of<uint8_t>(m, r);
+        const uint32_t block = c.c0 >> 7;
+        if constexpr (kA == kWide) {
+            if (!c.any()) return;
+            copy_async(word(n, 0), row + c.c0, 8);
+            copy_async(word(n, 0) + 8, ckpt_scales(row, s) + block, 4);
+        } else {
+            const uint32_t at = (c.c0 & ~(kWarpCols - 1)) + 4u * (threadIdx.x & 31u);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (at + 128u * k < s.code_bytes)
+                    copy_async(word(n, 0) + 4 * k, row + at + 128u * k, 4);
+                if (block + k < s.blocks)
+                    copy_async(word(n, 0) + 8 + 4 * k, ckpt_scales(row, s) + block + k, 4);
+            }
+        }
     }
-    // values of row r, from the slot that copy_row filled
+    // values of row r, from the slot that copy filled; every lane of the warp calls it
     template <int kA>
-    __device__ __forceinline__ Raw<T> get_row(uint32_t n, const Rows& m, bool codes,
-                                              const CkptShape& s, uint32_t r,
-                                              const Cols<kA>& c) const {
-        if (kA == kNarrow && codes) return load_codes<T, kA>(row_of<uint8_t>(m, r), s, c);
+    __device__ __forceinline__ Raw<T> get(uint32_t n, const Rows& m, uint32_t r,
+                                          const Cols<kA>& c) const {
         Raw<T> v = get(n);
-        if (codes) v.w[3] = v.w[2];
+        if constexpr (kA == kNarrow && sizeof(T) == 2) {
+            if (reinterpret_cast<uintptr_t>(row_of<T>(m, r)) & 2u) {   // halves of two words
+                const uint32_t lane = threadIdx.x & 31u;
+                uint32_t behind = 0;
+                if (lane == 0)
+                    asm volatile("ld.shared.b32 %0, [%1];"
+                                 : "=r"(behind)
+                                 : "r"(extra + n * (threads / 8))
+                                 : "memory");
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t give = lane == 0 ? (k < 3 ? v.w[k < 3 ? k + 1 : 3] : behind) : v.w[k];
+                    const uint32_t next = __shfl_sync(0xffffffffu, give, (lane + 1u) & 31u);
+                    w[k] = v.w[k] >> 16 | next << 16;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v.w[k] = w[k];
+            }
+            if (c.mask != 0xffu) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v.w[k] &= (c.mask >> (2 * k) & 1u ? 0xffffu : 0u) |
+                              (c.mask >> (2 * k + 1) & 1u ? 0xffff0000u : 0u);
+            }
+        }
+        return v;
+    }
+    template <int kA>
+    __device__ __forceinline__ Raw<T> get_row(uint32_t n, const Rows& m, bool codes, uint32_t r,
+                                              const Cols<kA>& c) const {
+        if (!codes) return get<kA>(n, m, r, c);
+        Raw<T> v = get(n);
+        if constexpr (kA == kWide) {
+            v.w[3] = v.w[2];
+        } else {
+            const uint32_t lane = threadIdx.x & 31u;
+            uint32_t pair[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t word = __shfl_sync(0xffffffffu, v.w[k / 2], (16 * k + (lane >> 1)) & 31u);
+                pair[k] = word >> 16 * (lane & 1u) & 0xffffu;
+                // missing columns: q = 0 (the second of a pair is padding then)
+                if (!(c.mask >> (2 * k) & 1u)) pair[k] = 0x8080u;
+            }
+            v.w[0] = pair[0] | pair[1] << 16;
+            v.w[1] = pair[2] | pair[3] << 16;
+        }
         return v;
     }
 };
-
-// Whether rows travel through slots: 16-bit values that cannot move as 16 bytes go through
-// registers, one row ahead.
-template <typename T, int kA>
-constexpr bool piped() { return kA == kWide || sizeof(T) == 4; }
 
 // Let a kernel use up to `most` bytes of dynamic shared memory on device `dev`, and tell how many
 // of its CTAs (threads, smem) an SM holds at once. Asked once per host thread and shape.

@@ -63,16 +63,12 @@ BackGeom back_geom(uint32_t rows, uint64_t cols, uint32_t group_rows, uint32_t l
 template <typename T, int kA, bool kPost, bool kGate, int G>
 struct BackShape {
     static constexpr bool kHeavy = kPost || kGate;
-    static constexpr int kWarps = kA == kNarrow && sizeof(T) == 2 && kPost && kGate ? 8
-                                  : sizeof(T) == 4 || G == 2                      ? 12
-                                                                                  : 16;
+    static constexpr int kWarps = sizeof(T) == 4 || G == 2 ? 12 : 16;
     static constexpr uint32_t kOps = kHeavy ? 5 : 4;       // y, du, dy, gate, h
     static constexpr uint32_t kVectors = kHeavy ? 3 : 1;   // pre_w, post_w, post_b
-    static constexpr bool kPipe = piped<T, kA>();
-    static constexpr uint32_t kDepth = !kPipe ? 0 : sizeof(T) == 4 ? 2 : G == 2 ? 3 : 4;   // rows on the way
+    static constexpr uint32_t kDepth = sizeof(T) == 4 ? 2 : G == 2 ? 3 : 4;   // rows on the way
     static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
-    static constexpr size_t kThreadBytes = (size_t)kSlots * 8 * sizeof(T);
-    static constexpr size_t kBytes = kThreadBytes * 32 * kWarps +
+    static constexpr size_t kBytes = (size_t)kSlots * (8 * sizeof(T) * 32 + 4) * kWarps +
                                      (size_t)(kPost && kGate ? 2 * G : 1) * kWarps * 1024 + 4096;
     static_assert(kBytes <= 227 * 1024, "shared memory of one CTA");
 };
@@ -152,30 +148,20 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
 
     // the vectors, and rows on their way, in this thread's slots of shared memory
     extern __shared__ uint4 dynamic[];
-    const Slots<T> slots{smem_addr(dynamic) + threadIdx.x * 16u, blockDim.x};
-    Raw<T> ry[G], rh[G], rdu[G], rdy[G];
+    const Slots<T> slots(smem_addr(dynamic), S::kSlots);
     auto fetch = [&](uint32_t r, uint32_t stage) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            if constexpr (S::kPipe) {
-                const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
-                if (has_du) {
-                    slots.template copy_row<kA>(n, p.x, y_codes, p.ck, r, c[i]);
-                    slots.template copy<kA>(n + G, row_of<T>(p.du, r), c[i]);
-                }
-                if (p.dy.p) slots.template copy<kA>(n + 2 * G, row_of<T>(p.dy, r), c[i]);
-                if (p.gate_rows)
-                    slots.template copy<kA>(n + 3 * G, row_of<T>(p.gate, r / p.gate_rows), c[i]);
-                if (kPost || kGate)
-                    slots.template copy_row<kA>(n + 4 * G, p.h, h_codes, p.ck, r, c[i]);
-            } else {
-                if (has_du) {
-                    ry[i] = load_row<T, kA>(p.x, y_codes, p.ck, r, c[i]);
-                    rdu[i] = load_raw<T, kA>(row_of<T>(p.du, r), c[i]);
-                }
-                if (p.dy.p) rdy[i] = load_raw<T, kA>(row_of<T>(p.dy, r), c[i]);
-                if (kPost || kGate) rh[i] = load_row<T, kA>(p.h, h_codes, p.ck, r, c[i]);
+            const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
+            if (has_du) {
+                slots.template copy_row<kA>(n, p.x, y_codes, p.ck, r, c[i]);
+                slots.template copy<kA>(n + G, row_of<T>(p.du, r), c[i]);
             }
+            if (p.dy.p) slots.template copy<kA>(n + 2 * G, row_of<T>(p.dy, r), c[i]);
+            if (p.gate_rows)
+                slots.template copy<kA>(n + 3 * G, row_of<T>(p.gate, r / p.gate_rows), c[i]);
+            if (kPost || kGate)
+                slots.template copy_row<kA>(n + 4 * G, p.h, h_codes, p.ck, r, c[i]);
         }
     };
     auto vector = [&](int n, int i, const void* v, float none, F8& out) {
@@ -197,45 +183,35 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
                 if (vectors[n]) slots.put(n * G + i, load_raw<T, kA>((const T*)vectors[n], c[i]));
         }
     }
-    constexpr uint32_t kLoads = S::kPipe ? S::kDepth : 1;   // rows ahead
     Walk in(cluster * g.teams + team), at = in;
     in.open(g, p.rows);
     at.open(g, p.rows);
 #pragma unroll
-    for (uint32_t k = 0; k < kLoads; ++k) {
+    for (uint32_t k = 0; k < S::kDepth; ++k) {
         if (in.row < in.end) {
             fetch(in.row, k);
             in.next(g, p.rows);
         }
-        if (S::kPipe) copy_commit();
+        copy_commit();
     }
     uint32_t stage = 0;
     while (at.row < at.end) {
         const uint32_t r = at.row, unit = at.unit;
         F8 y[G], h[G], du[G], gy[G], gate[G];
-        if (S::kPipe) copy_wait<kLoads - 1>();
+        copy_wait<S::kDepth - 1>();
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            if constexpr (S::kPipe) {
-                const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
-                if (has_du) {
-                    widen_row<T>(slots.template get_row<kA>(n, p.x, y_codes, p.ck, r, c[i]),
-                                 y_codes, y[i]);
-                    widen<T>(slots.get(n + G), du[i]);
-                }
-                if (p.dy.p) widen<T>(slots.get(n + 2 * G), gy[i]);
-                if (p.gate_rows) widen<T>(slots.get(n + 3 * G), gate[i]);
-                if (kPost || kGate)
-                    widen_row<T>(slots.template get_row<kA>(n + 4 * G, p.h, h_codes, p.ck, r, c[i]),
-                                 h_codes, h[i]);
-            } else {
-                if (has_du) {
-                    widen_row<T>(ry[i], y_codes, y[i]);
-                    widen<T>(rdu[i], du[i]);
-                }
-                if (p.dy.p) widen<T>(rdy[i], gy[i]);
-                if (kPost || kGate) widen_row<T>(rh[i], h_codes, h[i]);
+            const uint32_t n = S::kVectors * G + stage * S::kOps * G + i;
+            if (has_du) {
+                widen_row<T>(slots.template get_row<kA>(n, p.x, y_codes, r, c[i]), y_codes, y[i]);
+                widen<T>(slots.template get<kA>(n + G, p.du, r, c[i]), du[i]);
             }
+            if (p.dy.p) widen<T>(slots.template get<kA>(n + 2 * G, p.dy, r, c[i]), gy[i]);
+            if (p.gate_rows)
+                widen<T>(slots.template get<kA>(n + 3 * G, p.gate, r / p.gate_rows, c[i]), gate[i]);
+            if (kPost || kGate)
+                widen_row<T>(slots.template get_row<kA>(n + 4 * G, p.h, h_codes, r, c[i]), h_codes,
+                             h[i]);
             if (!p.dy.p) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) gy[i][k] = 0;
@@ -246,10 +222,8 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
             fetch(in.row, stage);
             in.next(g, p.rows);
         }
-        if (S::kPipe) {
-            copy_commit();
-            stage = stage + 1 == S::kDepth ? 0 : stage + 1;
-        }
+        copy_commit();
+        stage = stage + 1 == S::kDepth ? 0 : stage + 1;
 
         if (pre_layer || post_layer) {
             float s[2] = {0.0f, 0.0f};
@@ -340,8 +314,6 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
                     }
                 }
                 if (p.gate_rows) {
-                    if (!S::kPipe)
-                        widen<T>(load_raw<T, kA>(row_of<T>(p.gate, r / p.gate_rows), c[i]), gate[i]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) gy[i][k] = f2_mul(gy[i][k], gate[i][k]);
                 }
@@ -503,9 +475,9 @@ cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, Bac
     if (a.rows == 0) return cudaSuccess;
     auto kernel = join_back_kernel<T, kA, kPost, kGate, G>;
     const unsigned threads = 32 * g.warps * g.teams;
-    const size_t smem = S::kThreadBytes * threads;
+    const size_t smem = Slots<T>::bytes(S::kSlots, threads);
     int ctas = 1;
-    const cudaError_t e = resident(kernel, di.dev, threads, smem, S::kThreadBytes * 32 * S::kWarps,
+    const cudaError_t e = resident(kernel, di.dev, threads, smem, Slots<T>::bytes(S::kSlots, 32 * S::kWarps),
                                    &ctas);
     if (e != cudaSuccess) return e;
     const bool used = g.clusters > 1 || (a.dgate.p && g.parts > 1);
