@@ -733,6 +733,9 @@ void zero_sched_destroy(zero_sched* s);
  *   scales; zeros up to a multiple of 32.
  * A record holds a whole row: any range of rows is a checkpoint of its own (row r0's address is
  * base + r0*ZERO_CKPT_ROW_BYTES(cols)), so checkpoints can be split among ranks by rows.
+ * The calls of this section and the next are ordinary stream-ordered work: each waits for all
+ * work before it on its stream. Between zero_overlap_begin and zero_overlap_end they count as
+ * other work; close the region before a call of it reads what they write.
  * ---------------------------------------------------------------------------------------- */
 #define ZERO_CKPT_CODE_BYTES(cols) (((uint64_t)(cols) + 15u) / 16u * 16u)
 #define ZERO_CKPT_ROW_BYTES(cols) \
@@ -810,11 +813,12 @@ zero_status zero_ckpt_wgrad_q8(uint64_t tokens, uint64_t out_features, uint64_t 
  *           zero_ckpt_save_q8 writes for them; save_h needs h as a matrix; u needs a pre_norm.
  * Matrices: dtype, element-aligned, row strides ld* in elements (>= cols); vectors (post_w ...)
  * contiguous; checkpoints 16-byte aligned. y may be x itself (same address and stride); no other
- * output may overlap an input or another output.
+ * output may overlap an input or another output. 16-byte aligned rows of a multiple of 8 columns
+ * take the wide accesses; 16-bit rows that are only 2-byte aligned are read by the 4-byte words
+ * they overlap (at a row's ends such a word holds two bytes of its neighbour, which are ignored).
  * Errors: ZERO_EINVAL (the rules above, cols > ZERO_JOIN_MAX_COLS, rows or a row's stride in
  * bytes at or above 2^31, unknown dtype or norm, eps negative or not finite, scales not finite,
- * overlap), ZERO_EALIGN, ZERO_ECUDA. rows or
- * cols == 0 launches nothing.
+ * overlap), ZERO_EALIGN, ZERO_ECUDA. rows or cols == 0 launches nothing.
  * ---------------------------------------------------------------------------------------- */
 #define ZERO_JOIN_MAX_COLS 16384
 
