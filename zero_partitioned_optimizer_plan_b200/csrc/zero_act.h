@@ -68,6 +68,13 @@ cudaError_t launch_ckpt_load(uint64_t rows, const CkptShape& s, int dtype, const
                              const Mat& out, cudaStream_t stream);
 cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream);
 cudaError_t launch_join_backward(const JoinArgs& a, int dtype, void* ws, cudaStream_t stream);
+// One source per type (zero_join_*.cu).
+cudaError_t join_f16(const JoinArgs& a, cudaStream_t stream);
+cudaError_t join_bf16(const JoinArgs& a, cudaStream_t stream);
+cudaError_t join_f32(const JoinArgs& a, cudaStream_t stream);
+cudaError_t join_back_f16(const JoinArgs& a, float* ws, cudaStream_t stream);
+cudaError_t join_back_bf16(const JoinArgs& a, float* ws, cudaStream_t stream);
+cudaError_t join_back_f32(const JoinArgs& a, float* ws, cudaStream_t stream);
 
 struct WgradArgs {
     uint64_t tokens;

@@ -7,6 +7,8 @@
 //
 // A norm's statistics need one sum for RMS (of z^2) and two in turn for LayerNorm (of z, then of
 // (z - mean)^2: the difference of large squares would lose the variance of a row with a mean).
+#pragma once
+
 #include "zero_join.cuh"
 
 namespace zk {
@@ -94,10 +96,13 @@ struct ForwardShape {
     static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
 };
 
-template <typename T, int kA, int G, int kW>
+// kAll: a call with x and h as matrices and y and u asked for (see zero_join_back.cuh's kUse).
+template <typename T, int kA, int G, int kW, bool kAll>
 __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && kA == kWide ? 3 : 2)
     join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
     using S = ForwardShape<T, kA, G>;
+    const bool x_codes = !kAll && p.x_codes, h_codes = !kAll && p.h_codes;
+    const bool branch = kAll || p.has_branch, has_y = kAll || p.y.p, has_u = kAll || p.u.p;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
     const uint32_t warp = threadIdx.x >> 5, team = warp / warps, teams = (blockDim.x >> 5) / warps;
     uint32_t rank = 0;
@@ -118,8 +123,8 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
-            slots.template copy_row<kA>(n, p.x, p.x_codes, p.ck, r, c[g]);
-            if (p.has_branch) slots.template copy_row<kA>(n + G, p.h, p.h_codes, p.ck, r, c[g]);
+            slots.template copy_row<kA>(n, p.x, x_codes, p.ck, r, c[g]);
+            if (branch) slots.template copy_row<kA>(n + G, p.h, h_codes, p.ck, r, c[g]);
             if (p.gate_rows)
                 slots.template copy<kA>(n + 2 * G, row_of<T>(p.gate, r / p.gate_rows), c[g]);
         }
@@ -147,8 +152,8 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const uint32_t n = (S::kVectors + stage * S::kOps) * G + g;
-            rx[g] = slots.template get_row<kA>(n, p.x, p.x_codes, r, c[g]);
-            if (p.has_branch) rh[g] = slots.template get_row<kA>(n + G, p.h, p.h_codes, r, c[g]);
+            rx[g] = slots.template get_row<kA>(n, p.x, x_codes, r, c[g]);
+            if (branch) rh[g] = slots.template get_row<kA>(n + G, p.h, h_codes, r, c[g]);
             if (p.gate_rows)
                 rg[g] = slots.template get<kA>(n + 2 * G, p.gate, r / p.gate_rows, c[g]);
         }
@@ -162,10 +167,10 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
             if (first == 0) save_pad(row, p.ck, t.lane);
         }
         F8 y[G];
-        if (p.has_branch) {
+        if (branch) {
             F8 h[G];
 #pragma unroll
-            for (int g = 0; g < G; ++g) widen_row<T>(rh[g], p.h_codes, h[g]);
+            for (int g = 0; g < G; ++g) widen_row<T>(rh[g], h_codes, h[g]);
             if (p.post != ZERO_NORM_NONE) {
                 const float hr = centre<kA, G>(t, p.post, p.post_eps, inv_cols, c, h);
 #pragma unroll
@@ -183,7 +188,7 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                widen_row<T>(rx[g], p.x_codes, y[g]);
+                widen_row<T>(rx[g], x_codes, y[g]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     y[g][k] = f2_fma(both(p.bs), h[g][k], f2_mul(both(p.rs), y[g][k]));
@@ -191,17 +196,17 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
         } else {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                widen_row<T>(rx[g], p.x_codes, y[g]);
+                widen_row<T>(rx[g], x_codes, y[g]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[g][k] = f2_mul(both(p.rs), y[g][k]);
             }
         }
-        if (p.y.p || p.save_y.p) {
+        if (has_y || p.save_y.p) {
             Raw<T> ry[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 ry[g] = narrow<T>(y[g]);
-                if (p.y.p) store_raw<T, kA>(row_of<T>(p.y, r), c[g], ry[g]);
+                if (has_y) store_raw<T, kA>(row_of<T>(p.y, r), c[g], ry[g]);
             }
             if (p.save_y.p) {
                 uint8_t* row = row_of<uint8_t>(p.save_y, r);
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
                 if (first == 0) save_pad(row, p.ck, t.lane);
             }
         }
-        if (p.u.p) {
+        if (has_u) {
             const float yr = centre<kA, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
@@ -228,7 +233,8 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
     warps = (warps + ctas - 1) / ctas;
     const uint32_t teams = ctas == 1 ? kW / warps : 1;
     const unsigned threads = 32 * warps * teams;
-    auto kernel = join_kernel<T, kA, G, kW>;
+    const bool all = kA == kWide && !a.x_codes && !a.h_codes && a.has_branch && a.y.p && a.u.p;
+    auto kernel = all ? join_kernel<T, kA, G, kW, kA == kWide> : join_kernel<T, kA, G, kW, false>;
     constexpr uint32_t kSlots = ForwardShape<T, kA, G>::kSlots;
     const size_t smem = Slots<T>::bytes(kSlots, threads);
     int per_sm = 1;
@@ -271,11 +277,4 @@ cudaError_t run_join(const JoinArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
-
-cudaError_t launch_join(const JoinArgs& a, int dtype, cudaStream_t stream) {
-    return dtype == ZERO_F16    ? run_join<__half>(a, stream)
-           : dtype == ZERO_BF16 ? run_join<bf16>(a, stream)
-                                : run_join<float>(a, stream);
-}
-
 }  // namespace zk
