@@ -110,10 +110,12 @@ __host__ __device__ __forceinline__ uint64_t vector_partials(uint32_t cols) {
     return (uint64_t)kMaxParts * 4 * cols;
 }
 
-// kUse: kAny, or a call with every gradient matrix (dy, du in, dx, dh out) and the saved rows all
-// checkpoints (kCodes) or all matrices (kMatrices): without the questions which are there, the
-// kernel issues a fifth fewer instructions (16384 x 2048 fp16: 113 us with them, 95 without).
-enum Use { kAny = 0, kCodes = 1, kMatrices = 2 };
+// kUse: kAny, or what of a call is known beforehand: every gradient matrix (dy, du in, dx, dh out)
+// is there, the saved rows are all checkpoints (kCodes) or all matrices, the norms are all
+// LayerNorms (kLayer) or all RMS, and there is a gate exactly if its gradient is asked for.
+// Without the questions in its rows the kernel takes a fifth less time (16384 x 2048 fp16: 113 us
+// with them).
+enum Use { kAny = 0, kUsual = 1, kCodes = 2, kLayer = 4 };
 
 template <typename T, int kA, bool kPost, bool kGate, int G, int kUse>
 __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps, 1)
@@ -140,10 +142,12 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
         c[i] = Cols<kA>((i * g.ctas + rank) * g.warps + t.warp, t.lane, p.cols);
     const bool has_du = kUse != kAny || p.du.p, has_dy = kUse != kAny || p.dy.p;
     const bool has_dx = kUse != kAny || p.dx.p, has_dh = kUse != kAny || p.dh.p;
-    const bool y_codes = kUse == kAny ? p.x_codes : kUse == kCodes;
-    const bool h_codes = kUse == kAny ? p.h_codes : kUse == kCodes;
-    const bool pre_layer = has_du && p.pre == ZERO_NORM_LAYER;
-    const bool post_layer = kPost && p.post == ZERO_NORM_LAYER;
+    const bool y_codes = kUse == kAny ? p.x_codes : (kUse & kCodes) != 0;
+    const bool h_codes = kUse == kAny ? p.h_codes : (kUse & kCodes) != 0;
+    const bool has_gate = kUse == kAny ? p.gate_rows != 0 : kGate;
+    const bool pre_layer = kUse == kAny ? has_du && p.pre == ZERO_NORM_LAYER : (kUse & kLayer) != 0;
+    const bool post_layer =
+        kPost && (kUse == kAny ? p.post == ZERO_NORM_LAYER : (kUse & kLayer) != 0);
     F8 sum_pw[G] = {}, sum_pb[G] = {}, sum_qw[G] = {}, sum_qb[G] = {};
     if (kBoth) {
 #pragma unroll
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
                 slots.template copy<kA>(n + G, row_of<T>(p.du, r), c[i]);
             }
             if (has_dy) slots.template copy<kA>(n + 2 * G, row_of<T>(p.dy, r), c[i]);
-            if (p.gate_rows)
+            if (has_gate)
                 slots.template copy<kA>(n + 3 * G, row_of<T>(p.gate, r / p.gate_rows), c[i]);
             if (kPost || kGate)
                 slots.template copy_row<kA>(n + 4 * G, p.h, h_codes, p.ck, r, c[i]);
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
                 widen<T>(slots.template get<kA>(n + G, p.du, r, c[i]), du[i]);
             }
             if (has_dy) widen<T>(slots.template get<kA>(n + 2 * G, p.dy, r, c[i]), gy[i]);
-            if (p.gate_rows)
+            if (has_gate)
                 widen<T>(slots.template get<kA>(n + 3 * G, p.gate, r / p.gate_rows, c[i]), gate[i]);
             if (kPost || kGate)
                 widen_row<T>(slots.template get_row<kA>(n + 4 * G, p.h, h_codes, r, c[i]), h_codes,
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
                         if (kPost) sum_qb[i][k] = f2_add(sum_qb[i][k], gy[i][k]);
                     }
                 }
-                if (p.gate_rows) {
+                if (has_gate) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) gy[i][k] = f2_mul(gy[i][k], gate[i][k]);
                 }
@@ -498,13 +502,20 @@ template <typename T, int kA, bool kPost, bool kGate, int G>
 cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, BackGeom* g,
                             cudaStream_t stream) {
     if constexpr (kA == kWide) {
-        const bool all = a.dy.p && a.du.p && a.dx.p && a.dh.p;
         const bool h = kPost || kGate;
-        if (sizeof(T) == 2 && all && a.x_codes && (!h || a.h_codes))
-            return run_back_use<T, kA, kPost, kGate, G, sizeof(T) == 2 ? kCodes : kAny>(a, di, ws, g,
-                                                                                      stream);
-        if (all && !a.x_codes && (!h || !a.h_codes))
-            return run_back_use<T, kA, kPost, kGate, G, kMatrices>(a, di, ws, g, stream);
+        const bool usual = a.dy.p && a.du.p && a.dx.p && a.dh.p && (!h || a.h_codes == a.x_codes) &&
+                           (!kPost || a.post == a.pre) && (kGate || !a.gate.p);
+        const bool layer = a.pre == ZERO_NORM_LAYER;
+        if (usual && !a.x_codes)
+            return layer ? run_back_use<T, kA, kPost, kGate, G, kUsual | kLayer>(a, di, ws, g, stream)
+                         : run_back_use<T, kA, kPost, kGate, G, kUsual>(a, di, ws, g, stream);
+        if constexpr (sizeof(T) == 2) {
+            if (usual)
+                return layer ? run_back_use<T, kA, kPost, kGate, G, kUsual | kCodes | kLayer>(
+                                   a, di, ws, g, stream)
+                             : run_back_use<T, kA, kPost, kGate, G, kUsual | kCodes>(a, di, ws, g,
+                                                                                     stream);
+        }
     }
     return run_back_use<T, kA, kPost, kGate, G, kAny>(a, di, ws, g, stream);
 }

@@ -96,13 +96,21 @@ struct ForwardShape {
     static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
 };
 
-// kAll: a call with x and h as matrices and y and u asked for (see zero_join_back.cuh's kUse).
-template <typename T, int kA, int G, int kW, bool kAll>
+// kUse: kAny, or what of a call is known beforehand (without the questions in its rows the kernel
+// takes an eighth less time): x and h are matrices, y and u are asked for, and the norms are RMS
+// or LayerNorms (kLayer), with one after the block (kPost) or none.
+enum Known { kAny = 0, kUsual = 1, kPost = 2, kLayer = 4 };
+
+template <typename T, int kA, int G, int kW, int kUse>
 __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && kA == kWide ? 3 : 2)
     join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
     using S = ForwardShape<T, kA, G>;
+    constexpr bool kAll = kUse != kAny;
     const bool x_codes = !kAll && p.x_codes, h_codes = !kAll && p.h_codes;
     const bool branch = kAll || p.has_branch, has_y = kAll || p.y.p, has_u = kAll || p.u.p;
+    constexpr int kind = kUse & kLayer ? ZERO_NORM_LAYER : ZERO_NORM_RMS;
+    const int post = !kAll ? p.post : kUse & kPost ? kind : ZERO_NORM_NONE;
+    const int pre = kAll ? kind : p.pre;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
     const uint32_t warp = threadIdx.x >> 5, team = warp / warps, teams = (blockDim.x >> 5) / warps;
     uint32_t rank = 0;
@@ -171,8 +179,8 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
             F8 h[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) widen_row<T>(rh[g], h_codes, h[g]);
-            if (p.post != ZERO_NORM_NONE) {
-                const float hr = centre<kA, G>(t, p.post, p.post_eps, inv_cols, c, h);
+            if (post != ZERO_NORM_NONE) {
+                const float hr = centre<kA, G>(t, post, p.post_eps, inv_cols, c, h);
 #pragma unroll
                 for (int g = 0; g < G; ++g)
                     scale_shift<T, kA, G>(slots, g, c[g], hr, p.post_w, p.post_b, h[g]);
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
             }
         }
         if (has_u) {
-            const float yr = centre<kA, G>(t, p.pre, p.pre_eps, inv_cols, c, y);
+            const float yr = centre<kA, G>(t, pre, p.pre_eps, inv_cols, c, y);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 scale_shift<T, kA, G>(slots, 2 * G + g, c[g], yr, p.pre_w, p.pre_b, y[g]);
@@ -233,8 +241,19 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
     warps = (warps + ctas - 1) / ctas;
     const uint32_t teams = ctas == 1 ? kW / warps : 1;
     const unsigned threads = 32 * warps * teams;
-    const bool all = kA == kWide && !a.x_codes && !a.h_codes && a.has_branch && a.y.p && a.u.p;
-    auto kernel = all ? join_kernel<T, kA, G, kW, kA == kWide> : join_kernel<T, kA, G, kW, false>;
+    auto kernel = join_kernel<T, kA, G, kW, kAny>;
+    if constexpr (kA == kWide) {
+        if (!a.x_codes && !a.h_codes && a.has_branch && a.y.p && a.u.p &&
+            (a.post == ZERO_NORM_NONE || a.post == a.pre)) {
+            const bool layer = a.pre == ZERO_NORM_LAYER;
+            if (a.post == ZERO_NORM_NONE)
+                kernel = layer ? join_kernel<T, kA, G, kW, kUsual | kLayer>
+                               : join_kernel<T, kA, G, kW, kUsual>;
+            else
+                kernel = layer ? join_kernel<T, kA, G, kW, kUsual | kPost | kLayer>
+                               : join_kernel<T, kA, G, kW, kUsual | kPost>;
+        }
+    }
     constexpr uint32_t kSlots = ForwardShape<T, kA, G>::kSlots;
     const size_t smem = Slots<T>::bytes(kSlots, threads);
     int per_sm = 1;
