@@ -217,6 +217,8 @@ def test_binding_checks_shapes_and_types():
                 lambda: lz.zero_ckpt_save_q8(4, 64, x, ck[:3], stream=0),
                 lambda: lz.zero_ckpt_save_q8(4, 64, x, ck.float(), stream=0),
                 lambda: lz.zero_ckpt_save_q8(4, 64, at(0), ck, stream=0),
+                lambda: lz.zero_ckpt_save_q8(4, 64, x, ck, stream=0),           # host memory
+                lambda: lz.zero_ckpt_load_q8(4, 64, ck, at(0), dtype=0, stream=0),
                 lambda: lz.zero_block_join(4, 64, x=x, h=x.float(), y=x, stream=0),
                 lambda: lz.zero_block_join(4, 64, x=x, u=x.clone(), pre_norm="rms",
                                            pre_w=x[0, :63].clone(), stream=0),

@@ -320,6 +320,34 @@ def test_join_backward(rows, cols, T):
                     A.CHAIN if n in ("dx", "dh") else A.CHAIN + rows)
 
 
+@pytest.mark.parametrize("T,rows,cols", [(F16, 400, 8192), (F16, 330, 16384), (BF16, 350, 5000),
+                                         (F32, 300, 4096), (F32, 170, 16384), (F16, 210, 5263)])
+@pytest.mark.parametrize("post,pre,gate_rows", [("rms", "rms", 100), ("none", "layer", 0),
+                                                ("layer", "layer", 0)])
+def test_wide_rows(rows, cols, T, post, pre, gate_rows):
+    """Rows that several CTAs share, several rows one after the other per cluster."""
+    d, ref, x, h = _boundary(rows, cols, T, post, pre, gate_rows, True, 60)
+    y, u = torch.empty_like(x), torch.empty_like(x)
+    sy, sh = _ckpt_buf(rows, cols), _ckpt_buf(rows, cols)
+    lz.zero_block_join(rows, cols, x=x, h=h, y=y, u=u, save_y=sy, save_h=sh, **d)
+    wy, wu, my, mu = A.join(ref, A.f64(x), A.f64(h))
+    A.close("y", y, wy, my, T, ROW_FWD)
+    A.close("u", u, wu, mu, T, A.CHAIN)
+    assert A.same_bytes(sy.cpu().numpy(), A.record(y.cpu().float().numpy()), cols)
+    dy, du = _mat(rows, cols, T, 1, 0.1), _mat(rows, cols, T, 2, 0.1)
+    names = ["dx", "dh", "dpre_w", "dpre_b"] + ["dpost_w", "dpost_b"] * (post != "none") + \
+        ["dgate"] * (gate_rows > 0)
+    if T is F32:
+        got, yv, hv = _back(d, rows, cols, T, y, h, dy, du, names), A.f64(y), A.f64(h)
+    else:
+        got = _back(d, rows, cols, T, sy, sh, dy, du, names)
+        yv, hv = (A.values(c.cpu().numpy(), cols).astype(np.float64) for c in (sy, sh))
+    want = A.back(ref, yv, hv, A.f64(dy), A.f64(du))
+    for n in names:
+        v, m = want[n]
+        A.close(n, got[n], v, m, T, A.CHAIN if n in ("dx", "dh") else A.CHAIN + rows)
+
+
 def test_join_backward_parts():
     """Any subset of the outputs and gradients: the same bits as from the full call."""
     rows, cols = 50, 384

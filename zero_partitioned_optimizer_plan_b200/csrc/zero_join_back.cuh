@@ -493,7 +493,9 @@ cudaError_t run_back_use(const JoinArgs& a, const DevInfo& di, float* ws, BackGe
     const cudaError_t e = resident(kernel, di.dev, threads, smem, Slots<T>::bytes(S::kSlots, 32 * S::kWarps),
                                    &ctas);
     if (e != cudaSuccess) return e;
-    const bool used = g.clusters > 1 || (a.dgate.p && g.parts > 1);
+    // a second kernel follows exactly if partial sums are left in the workspace
+    const bool used = ((a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b) && g.clusters > 1) ||
+                      (a.dgate.p && g.parts > 1);
     return launch_clusters(kernel, g.clusters, g.ctas, threads, smem, stream, a, g,
                            used ? ws : (float*)nullptr);
 }

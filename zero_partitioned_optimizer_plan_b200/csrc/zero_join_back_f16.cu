@@ -9,7 +9,7 @@ cudaError_t join_back_f16(const JoinArgs& a, float* ws, cudaStream_t stream) {
 }
 
 // Enough for every type and set of outputs: the vectors' partial sums, and a partial gate row
-// per team where a gate row's rows may be dealt to several.
+// per team (at least as many as units) where a gate row's rows may be dealt to several.
 uint64_t join_workspace(uint64_t rows, uint64_t cols, uint64_t gate_rows) {
     if (cols == 0) return 0;
     uint64_t floats = vector_partials((uint32_t)cols);
@@ -20,7 +20,7 @@ uint64_t join_workspace(uint64_t rows, uint64_t cols, uint64_t gate_rows) {
                 const BackGeom g = back_geom((uint32_t)rows, cols,
                                              (uint32_t)(gate_rows < rows ? gate_rows : rows),
                                              chunks, warps, kMaxParts);
-                if (g.parts > 1 && g.units > most) most = g.units;
+                if (g.parts > 1 && g.clusters * g.teams > most) most = g.clusters * g.teams;
             }
         floats += most * cols;
     }

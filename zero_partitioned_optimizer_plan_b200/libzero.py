@@ -889,6 +889,8 @@ def _mat(x, rows: int, cols: int):
         return (int(x[0]), int(x[1])) if isinstance(x, tuple) else (int(x), cols)
     if shape != (rows, cols):
         raise TypeError(f"expected a {rows} x {cols} tensor, got {tuple(shape)}")
+    if not x.is_cuda:
+        raise TypeError("expected a tensor in device memory")
     if stride[1] != 1 and cols > 1:
         raise TypeError("the columns of a matrix must be adjacent")
     ld = stride[0]
@@ -898,8 +900,11 @@ def _mat(x, rows: int, cols: int):
 def _ckpt(x, rows: int, cols: int) -> int:
     if x is None:
         return 0
-    if hasattr(x, "data_ptr") and x.nbytes < rows * ckpt_row_bytes(cols):
-        raise TypeError("checkpoint buffer smaller than rows * ckpt_row_bytes(cols)")
+    if hasattr(x, "data_ptr"):
+        if x.nbytes < rows * ckpt_row_bytes(cols):
+            raise TypeError("checkpoint buffer smaller than rows * ckpt_row_bytes(cols)")
+        if not x.is_cuda:
+            raise TypeError("expected a checkpoint in device memory")
     return _ptr(x, 1)
 
 
@@ -910,8 +915,9 @@ def _vec(x, cols: int) -> int:
         n, ptr = x.numel(), x.data_ptr()
     except AttributeError:
         return int(x)
-    if n != cols or not x.is_contiguous():
-        raise TypeError(f"expected a contiguous vector of {cols} values, got {tuple(x.shape)}")
+    if n != cols or not x.is_contiguous() or not x.is_cuda:
+        raise TypeError(f"expected a contiguous vector of {cols} values in device memory, got "
+                        f"{tuple(x.shape)}")
     return ptr
 
 
