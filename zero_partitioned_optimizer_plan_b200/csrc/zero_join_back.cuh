@@ -110,12 +110,12 @@ __host__ __device__ __forceinline__ uint64_t vector_partials(uint32_t cols) {
     return (uint64_t)kMaxParts * 4 * cols;
 }
 
-// kUse: kAny, or what of a call is known beforehand: every gradient matrix (dy, du in, dx, dh out)
-// is there, the saved rows are all checkpoints (kCodes) or all matrices, the norms are all
-// LayerNorms (kLayer) or all RMS, and there is a gate exactly if its gradient is asked for.
-// Without the questions in its rows the kernel takes a fifth less time (16384 x 2048 fp16: 113 us
-// with them).
-enum Use { kAny = 0, kUsual = 1, kCodes = 2, kLayer = 4 };
+// kUse: kAny, or what of a call is known beforehand. kUsual: every gradient matrix (dy, du in, dx,
+// dh out) is there, the saved rows are all checkpoints (kCodes) or all matrices. kNorms: the norms
+// are all LayerNorms (kLayer) or all RMS, and there is a gate exactly if its gradient is asked
+// for. Without the questions in its rows the kernel takes a fifth less time (16384 x 2048 fp16:
+// 113 us with them, 95 without the first, 89 without both).
+enum Use { kAny = 0, kUsual = 1, kCodes = 2, kLayer = 4, kNorms = 8 };
 
 template <typename T, int kA, bool kPost, bool kGate, int G, int kUse>
 __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps, 1)
@@ -144,10 +144,10 @@ __global__ void __launch_bounds__(32 * BackShape<T, kA, kPost, kGate, G>::kWarps
     const bool has_dx = kUse != kAny || p.dx.p, has_dh = kUse != kAny || p.dh.p;
     const bool y_codes = kUse == kAny ? p.x_codes : (kUse & kCodes) != 0;
     const bool h_codes = kUse == kAny ? p.h_codes : (kUse & kCodes) != 0;
-    const bool has_gate = kUse == kAny ? p.gate_rows != 0 : kGate;
-    const bool pre_layer = kUse == kAny ? has_du && p.pre == ZERO_NORM_LAYER : (kUse & kLayer) != 0;
+    const bool has_gate = kUse & kNorms ? kGate : p.gate_rows != 0;
+    const bool pre_layer = kUse & kNorms ? (kUse & kLayer) != 0 : has_du && p.pre == ZERO_NORM_LAYER;
     const bool post_layer =
-        kPost && (kUse == kAny ? p.post == ZERO_NORM_LAYER : (kUse & kLayer) != 0);
+        kPost && (kUse & kNorms ? (kUse & kLayer) != 0 : p.post == ZERO_NORM_LAYER);
     F8 sum_pw[G] = {}, sum_pb[G] = {}, sum_qw[G] = {}, sum_qb[G] = {};
     if (kBoth) {
 #pragma unroll
@@ -503,21 +503,24 @@ cudaError_t run_back_use(const JoinArgs& a, const DevInfo& di, float* ws, BackGe
 template <typename T, int kA, bool kPost, bool kGate, int G>
 cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, BackGeom* g,
                             cudaStream_t stream) {
+    const bool h = kPost || kGate;
+    const bool usual = a.dy.p && a.du.p && a.dx.p && a.dh.p && (!h || a.h_codes == a.x_codes);
+    const bool norms = (!kPost || a.post == a.pre) && (kGate || !a.gate.p);
+    const bool layer = a.pre == ZERO_NORM_LAYER;
+    constexpr int kM = kUsual, kC = kUsual | kCodes;
     if constexpr (kA == kWide) {
-        const bool h = kPost || kGate;
-        const bool usual = a.dy.p && a.du.p && a.dx.p && a.dh.p && (!h || a.h_codes == a.x_codes) &&
-                           (!kPost || a.post == a.pre) && (kGate || !a.gate.p);
-        const bool layer = a.pre == ZERO_NORM_LAYER;
-        if (usual && !a.x_codes)
-            return layer ? run_back_use<T, kA, kPost, kGate, G, kUsual | kLayer>(a, di, ws, g, stream)
-                         : run_back_use<T, kA, kPost, kGate, G, kUsual>(a, di, ws, g, stream);
-        if constexpr (sizeof(T) == 2) {
-            if (usual)
-                return layer ? run_back_use<T, kA, kPost, kGate, G, kUsual | kCodes | kLayer>(
-                                   a, di, ws, g, stream)
-                             : run_back_use<T, kA, kPost, kGate, G, kUsual | kCodes>(a, di, ws, g,
-                                                                                     stream);
+        if (usual && norms && !a.x_codes)
+            return layer ? run_back_use<T, kA, kPost, kGate, G, kM | kNorms | kLayer>(a, di, ws, g, stream)
+                         : run_back_use<T, kA, kPost, kGate, G, kM | kNorms>(a, di, ws, g, stream);
+        if constexpr (sizeof(T) == 2) {   // (32-bit activations are rarely kept in 8 bits)
+            if (usual && norms)
+                return layer ? run_back_use<T, kA, kPost, kGate, G, kC | kNorms | kLayer>(a, di, ws, g, stream)
+                             : run_back_use<T, kA, kPost, kGate, G, kC | kNorms>(a, di, ws, g, stream);
         }
+    } else if (usual) {
+        if (!a.x_codes) return run_back_use<T, kA, kPost, kGate, G, kM>(a, di, ws, g, stream);
+        if constexpr (sizeof(T) == 2 && !kPost)   // (with a norm after the block: registers)
+            return run_back_use<T, kA, kPost, kGate, G, kC>(a, di, ws, g, stream);
     }
     return run_back_use<T, kA, kPost, kGate, G, kAny>(a, di, ws, g, stream);
 }

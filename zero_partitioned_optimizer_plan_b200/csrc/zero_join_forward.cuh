@@ -97,9 +97,9 @@ struct ForwardShape {
 };
 
 // kUse: kAny, or what of a call is known beforehand (without the questions in its rows the kernel
-// takes an eighth less time): x and h are matrices, y and u are asked for, and the norms are RMS
-// or LayerNorms (kLayer), with one after the block (kPost) or none.
-enum Known { kAny = 0, kUsual = 1, kPost = 2, kLayer = 4 };
+// takes an eighth less time). kUsual: x and h are matrices, y and u are asked for. kNorms: the
+// norms are RMS or LayerNorms (kLayer), with one after the block (kPost) or none.
+enum Known { kAny = 0, kUsual = 1, kPost = 2, kLayer = 4, kNorms = 8 };
 
 template <typename T, int kA, int G, int kW, int kUse>
 __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && kA == kWide ? 3 : 2)
@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && 
     const bool x_codes = !kAll && p.x_codes, h_codes = !kAll && p.h_codes;
     const bool branch = kAll || p.has_branch, has_y = kAll || p.y.p, has_u = kAll || p.u.p;
     constexpr int kind = kUse & kLayer ? ZERO_NORM_LAYER : ZERO_NORM_RMS;
-    const int post = !kAll ? p.post : kUse & kPost ? kind : ZERO_NORM_NONE;
-    const int pre = kAll ? kind : p.pre;
+    const int post = !(kUse & kNorms) ? p.post : kUse & kPost ? kind : ZERO_NORM_NONE;
+    const int pre = kUse & kNorms ? kind : p.pre;
     __shared__ float part[2][kMaxWarps * kMaxCluster][4];
     const uint32_t warp = threadIdx.x >> 5, team = warp / warps, teams = (blockDim.x >> 5) / warps;
     uint32_t rank = 0;
@@ -242,17 +242,20 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
     const uint32_t teams = ctas == 1 ? kW / warps : 1;
     const unsigned threads = 32 * warps * teams;
     auto kernel = join_kernel<T, kA, G, kW, kAny>;
+    const bool usual = !a.x_codes && !a.h_codes && a.has_branch && a.y.p && a.u.p;
     if constexpr (kA == kWide) {
-        if (!a.x_codes && !a.h_codes && a.has_branch && a.y.p && a.u.p &&
-            (a.post == ZERO_NORM_NONE || a.post == a.pre)) {
+        if (usual && (a.post == ZERO_NORM_NONE || a.post == a.pre)) {
+            constexpr int kU = kUsual | kNorms;
             const bool layer = a.pre == ZERO_NORM_LAYER;
             if (a.post == ZERO_NORM_NONE)
-                kernel = layer ? join_kernel<T, kA, G, kW, kUsual | kLayer>
-                               : join_kernel<T, kA, G, kW, kUsual>;
+                kernel = layer ? join_kernel<T, kA, G, kW, kU | kLayer>
+                               : join_kernel<T, kA, G, kW, kU>;
             else
-                kernel = layer ? join_kernel<T, kA, G, kW, kUsual | kPost | kLayer>
-                               : join_kernel<T, kA, G, kW, kUsual | kPost>;
+                kernel = layer ? join_kernel<T, kA, G, kW, kU | kPost | kLayer>
+                               : join_kernel<T, kA, G, kW, kU | kPost>;
         }
+    } else if (usual) {
+        kernel = join_kernel<T, kA, G, kW, kUsual>;
     }
     constexpr uint32_t kSlots = ForwardShape<T, kA, G>::kSlots;
     const size_t smem = Slots<T>::bytes(kSlots, threads);
