@@ -86,13 +86,15 @@ __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint3
 // A CTA has kW warps at most, 8 or (rows of more than 4096 columns) 16; still wider rows are
 // shared by the CTAs of a cluster.
 
-// Rows on the way: what lets two CTAs (three of one 16-bit chunk per lane) fit an SM.
+// Rows on the way: many for one chunk per lane. Two 16-bit chunks per lane take one row ahead,
+// which with their registers held down (forward_ctas) lets three CTAs fit an SM: 8192 x 4096 bf16 with
+// both checkpoints 127 us, 16384 x 2048 fp16 101; with three rows ahead and two CTAs 149 and 107.
 template <typename T, int kA, int G>
 struct ForwardShape {
     // post_w, post_b, pre_w, pre_b; two 32-bit chunks leave no room for them
     static constexpr uint32_t kVectors = sizeof(T) * G <= 4 ? 4 : 0;
     static constexpr uint32_t kOps = 3;       // x, h, gate
-    static constexpr uint32_t kDepth = sizeof(T) * G == 2 ? 4 : sizeof(T) * G == 4 ? 3 : 2;
+    static constexpr uint32_t kDepth = sizeof(T) == 2 ? (G == 1 ? 4 : 1) : (G == 1 ? 3 : 2);
     static constexpr uint32_t kSlots = (kVectors + kDepth * kOps) * G;
 };
 
@@ -101,8 +103,15 @@ struct ForwardShape {
 // norms are RMS or LayerNorms (kLayer), with one after the block (kPost) or none.
 enum Known { kAny = 0, kUsual = 1, kPost = 2, kLayer = 4, kNorms = 8 };
 
+// CTAs an SM holds at least.
 template <typename T, int kA, int G, int kW, int kUse>
-__global__ void __launch_bounds__(32 * kW, kW == 16 ? 1 : sizeof(T) * G == 2 && kA == kWide ? 3 : 2)
+constexpr int forward_ctas() {
+    if (kW == 16) return 1;
+    return sizeof(T) == 2 && kA == kWide && (G == 1 || kUse != kAny) ? 3 : 2;
+}
+
+template <typename T, int kA, int G, int kW, int kUse>
+__global__ void __launch_bounds__(32 * kW, forward_ctas<T, kA, G, kW, kUse>())
     join_kernel(const __grid_constant__ JoinArgs p, uint32_t warps, uint32_t ctas, float inv_cols) {
     using S = ForwardShape<T, kA, G>;
     constexpr bool kAll = kUse != kAny;
@@ -271,10 +280,9 @@ cudaError_t run_forward(const JoinArgs& a, const DevInfo& di, cudaStream_t strea
 }
 
 // Chunks per lane: two, so that the work per row that does not grow with the columns is shared by
-// more of them (16384 x 2048 fp16 with both checkpoints: 123 us, with one 146); one where a row
-// has three or fewer, where it has 32-bit values that move
-// singly, or where there are too few rows to
-// fill the device anyway.
+// more of them (16384 x 2048 fp16 with both checkpoints: 101 us, with one 131); one where a row
+// has three or fewer, where it has 32-bit values that move singly, or where there are too few rows
+// to fill the device anyway.
 template <typename T, int kA>
 cudaError_t run_forward_any(const JoinArgs& a, cudaStream_t stream) {
     DevInfo di;
