@@ -526,8 +526,8 @@ cudaError_t run_back_kernel(const JoinArgs& a, const DevInfo& di, float* ws, Bac
 }
 
 // Two chunks per lane for 16-bit rows wider than one in a boundary without a norm after the block
-// and a gate (16384 x 2048 fp16: 107 us, with one 112); with them the registers leave so few warps
-// that one is faster (8192 x 4096 bf16: 187 us, with two 198). The choice does not go by the
+// and a gate (16384 x 2048 fp16: 89 us, with one 93); with them the column sums of two chunks and
+// their rows on the way do not fit an SM with as many warps. The choice does not go by the
 // outputs asked for: dx and dh have the same bits with and without the others.
 template <typename T, int kA>
 cudaError_t run_back_any(const JoinArgs& a, const DevInfo& di, float* ws, BackGeom* g,
