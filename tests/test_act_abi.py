@@ -226,3 +226,20 @@ def test_binding_checks_shapes_and_types():
                                                     gate=x.clone(), stream=0)):
         with pytest.raises(TypeError):
             bad()
+
+
+HUGE = (1 << 64) - 1
+
+
+@pytest.mark.parametrize("gate_rows", [9, HUGE, HUGE - 6])
+def test_gate_of_more_rows_than_there_are(gate_rows):
+    """One gate row for every row, however large gate_rows is: it is checked like any other."""
+    kw = dict(gate_rows=gate_rows)
+    assert _join(gate=at(9, 1), **kw) == EALIGN
+    assert _join(gate=(at(9), 63), **kw) == EINVAL
+    assert _join(gate=at(2, 64), **kw) == EINVAL            # inside y
+    back = dict(kw, gate=at(15))
+    assert _back(dgate=at(14, 1), **back) == EALIGN
+    assert _back(dgate=(at(14), 63), **back) == EINVAL
+    assert _back(dgate=at(15), **back) == EINVAL            # the gate itself
+    assert _back(dgate=at(4, 128), **back) == EINVAL        # inside dx

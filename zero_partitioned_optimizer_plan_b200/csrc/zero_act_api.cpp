@@ -85,8 +85,9 @@ zero_status check_desc(const zero_block_desc* d) {
     return ZERO_OK;
 }
 
+// (any gate_rows: the sum rows + gate_rows may pass 64 bits)
 uint64_t gate_count(const zero_block_desc* d) {
-    return d->gate_rows ? (d->rows + d->gate_rows - 1) / d->gate_rows : 0;
+    return d->gate_rows && d->rows ? (d->rows - 1) / d->gate_rows + 1 : 0;
 }
 
 // The buffers of one boundary call: every one checked for its shape and alignment as it is
