@@ -243,3 +243,85 @@ def test_gate_of_more_rows_than_there_are(gate_rows):
     assert _back(dgate=(at(14), 63), **back) == EINVAL
     assert _back(dgate=at(15), **back) == EINVAL            # the gate itself
     assert _back(dgate=at(4, 128), **back) == EINVAL        # inside dx
+
+
+class OnDevice:
+    """What the binding reads of a device tensor. All lie at one address, so that the library refuses
+    every call that the binding lets through (its operands overlap)."""
+
+    def __init__(self, shape, dtype, device=1):
+        self.shape, self.dtype, self.index = shape, dtype, device
+        self.is_cuda = True
+        self.nbytes = self.numel() * self.element_size()
+
+    def stride(self):
+        return tuple(self.numel(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def numel(self, shape=None):
+        n = 1
+        for s in self.shape if shape is None else shape:
+            n *= s
+        return n
+
+    def data_ptr(self):
+        return at(0)
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+
+def test_binding_refuses_workspace_and_status_in_host_memory():
+    torch = pytest.importorskip("torch")
+    host, word = torch.zeros(64, dtype=torch.uint8), torch.zeros(1, dtype=torch.int32)
+    kw = dict(dtype=0, stream=0)
+    a = at(0)
+    for bad in (lambda: lz.zero_ckpt_wgrad_q8(1 << 16, 256, 256, a, a, a, a, workspace=host, **kw),
+                lambda: lz.zero_ckpt_wgrad_q8(64, 256, 256, a, a, a, word, **kw),
+                lambda: lz.zero_ckpt_wgrad_q8(64, 256, 256, a, a, a, a, workspace=a, **kw),  # size?
+                lambda: lz.zero_block_join_backward(4, 64, dy=a, du=a, y=a, dx=a, dpre_w=a,
+                                                    pre_norm="rms", workspace=host, **kw)):
+        before = lz.zero_kernel_launches()
+        with pytest.raises(TypeError):
+            bad()
+        assert lz.zero_kernel_launches() == before
+
+
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    """The calls run on the current device: a tensor of another one is refused, whichever operand it
+    is."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(lz, "_several_devices", True)
+    monkeypatch.setattr(lz, "_current_device", lambda: 1)
+    f16, u8 = torch.float16, torch.uint8
+    m, rec = (4, 64), (4, lz.ckpt_row_bytes(64))
+    shapes = dict(x=(m, f16), h=(m, f16), y=(m, f16), u=(m, f16), ck=(rec, u8), w=((64,), f16),
+                  gate=(m, f16), dw=((64, 64), f16), ws=((1 << 23,), u8),
+                  status=((1,), torch.int32))
+
+    def calls(o):
+        norms = dict(pre_norm="rms", post_norm="rms", pre_w=o["w"], gate=o["gate"], gate_rows=1,
+                     stream=0)
+        yield "x ck", lambda: lz.zero_ckpt_save_q8(4, 64, o["x"], o["ck"], stream=0)
+        yield "x ck", lambda: lz.zero_ckpt_load_q8(4, 64, o["ck"], o["x"], stream=0)
+        yield "x h y u ck w gate", lambda: lz.zero_block_join(
+            4, 64, x=o["x"], h=o["h"], y=o["y"], u=o["u"], save_y=o["ck"], **norms)
+        yield "x h y u w gate ws", lambda: lz.zero_block_join_backward(
+            4, 64, y=o["y"], h=o["h"], dy=o["x"], du=o["u"], dx=at(0), dpre_b=at(0),
+            workspace=o["ws"], **norms)
+        yield "x ck dw ws status", lambda: lz.zero_ckpt_wgrad_q8(
+            4, 64, 64, o["x"], o["ck"], o["dw"], o["status"], workspace=o["ws"], stream=0)
+
+    here = {k: OnDevice(*v) for k, v in shapes.items()}
+    for _, call in calls(here):
+        with pytest.raises(lz.ZeroError):
+            call()
+    for other in shapes:
+        for names, call in calls(dict(here, **{other: OnDevice(*shapes[other], device=0)})):
+            with pytest.raises(TypeError if other in names.split() else lz.ZeroError):
+                call()

@@ -878,6 +878,25 @@ def _dtype_of(xs, dtype) -> int:
     return dtype
 
 
+# The calls run on the current device. Where the process sees one device only, every device tensor
+# is on it and the question is not asked.
+_several_devices = None
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _elsewhere(x) -> bool:
+    """Is a device tensor on another device than the current one?"""
+    global _several_devices
+    if _several_devices is None:
+        import torch
+        _several_devices = torch.cuda.device_count() > 1
+    return _several_devices and x.get_device() != _current_device()
+
+
 def _mat(x, rows: int, cols: int):
     """(address, row stride) of a rows x cols operand: a tensor whose columns are adjacent (its
     rows may be strided), (address, stride), or an address of adjacent rows."""
@@ -889,8 +908,8 @@ def _mat(x, rows: int, cols: int):
         return (int(x[0]), int(x[1])) if isinstance(x, tuple) else (int(x), cols)
     if shape != (rows, cols):
         raise TypeError(f"expected a {rows} x {cols} tensor, got {tuple(shape)}")
-    if not x.is_cuda:
-        raise TypeError("expected a tensor in device memory")
+    if not x.is_cuda or (_several_devices is not False and _elsewhere(x)):
+        raise TypeError("expected a tensor in the current device's memory")
     if stride[1] != 1 and cols > 1:
         raise TypeError("the columns of a matrix must be adjacent")
     ld = stride[0]
@@ -903,8 +922,8 @@ def _ckpt(x, rows: int, cols: int) -> int:
     if hasattr(x, "data_ptr"):
         if x.nbytes < rows * ckpt_row_bytes(cols):
             raise TypeError("checkpoint buffer smaller than rows * ckpt_row_bytes(cols)")
-        if not x.is_cuda:
-            raise TypeError("expected a checkpoint in device memory")
+        if not x.is_cuda or (_several_devices is not False and _elsewhere(x)):
+            raise TypeError("expected a checkpoint in the current device's memory")
     return _ptr(x, 1)
 
 
@@ -915,16 +934,29 @@ def _vec(x, cols: int) -> int:
         n, ptr = x.numel(), x.data_ptr()
     except AttributeError:
         return int(x)
-    if n != cols or not x.is_contiguous() or not x.is_cuda:
-        raise TypeError(f"expected a contiguous vector of {cols} values in device memory, got "
-                        f"{tuple(x.shape)}")
+    if n != cols or not x.is_contiguous() or not x.is_cuda or \
+            (_several_devices is not False and _elsewhere(x)):
+        raise TypeError(f"expected a contiguous vector of {cols} values in the current device's "
+                        f"memory, got {tuple(x.shape)}")
     return ptr
+
+
+def _buf(x, elem_size: int | None = None) -> int:
+    """The address of a workspace or status word."""
+    if hasattr(x, "data_ptr") and (not x.is_cuda or
+                                   (_several_devices is not False and _elsewhere(x))):
+        raise TypeError("expected workspace and status in the current device's memory")
+    return _ptr(x, elem_size)
 
 
 def _nbytes(x, given=None) -> int:
     if given is not None:
         return given
-    return 0 if x is None else x.numel() * x.element_size()
+    if x is None:
+        return 0
+    if not hasattr(x, "data_ptr"):
+        raise TypeError("workspace_bytes is needed where the workspace is an address")
+    return x.numel() * x.element_size()
 
 
 def zero_ckpt_save_q8(rows: int, cols: int, x, ckpt, dtype: int | None = None, stream=None):
@@ -960,8 +992,8 @@ def zero_ckpt_wgrad_q8(tokens: int, out_features: int, in_features: int, dy, ckp
     pdw, lddw = _mat(dw, out_features, in_features)
     _check(_lib.zero_ckpt_wgrad_q8(tokens, out_features, in_features, _dtype_of((dy, dw), dtype),
                                    pdy, lddy, _ckpt(ckpt, tokens, in_features), pdw, lddw,
-                                   1 if accumulate else 0, _ptr(workspace),
-                                   _nbytes(workspace, workspace_bytes), _ptr(d_status, 4),
+                                   1 if accumulate else 0, _buf(workspace),
+                                   _nbytes(workspace, workspace_bytes), _buf(d_status, 4),
                                    _stream(stream)), "zero_ckpt_wgrad_q8")
 
 
@@ -1026,5 +1058,5 @@ def zero_block_join_backward(rows: int, cols: int, *, y=None, y_ckpt=None, h=Non
         *_mat(h, rows, cols), _ckpt(h_ckpt, rows, cols), *_mat(dy, rows, cols),
         *_mat(du, rows, cols), *_mat(dx, rows, cols), *_mat(dh, rows, cols),
         *_mat(dgate, gates, cols), _vec(dpost_w, cols), _vec(dpost_b, cols), _vec(dpre_w, cols),
-        _vec(dpre_b, cols), accumulate, _ptr(workspace), _nbytes(workspace, workspace_bytes),
+        _vec(dpre_b, cols), accumulate, _buf(workspace), _nbytes(workspace, workspace_bytes),
         _stream(stream)), "zero_block_join_backward")
