@@ -616,9 +616,11 @@ zero_status zero_selftest_timeout(uint32_t* d_status, zero_stream_t stream);
  * whole region as usual. Calls that take the plain-load kernels, and all other calls, stay
  * ordered. Other work enqueued on the stream inside the region must be ordinary launches,
  * copies, event records or event waits (a kernel that itself uses programmatic dependent
- * launch, as some libraries' kernels do, needs the region closed before it); an event recorded
- * after a call completes only when that call and every call before it have. The bucket
- * scheduler's calls (zero_sched_end_bucket on its stream) may sit in a region.
+ * launch, as some libraries' kernels do, needs the region closed before it; this library's
+ * activation calls use it too, in a form that waits for every call before them and lets none
+ * after them start early, and may sit inside); an event recorded after a call completes only when
+ * that call and every call before it have. The bucket scheduler's calls (zero_sched_end_bucket on
+ * its stream) may sit in a region.
  * Host-side state only (one flag per stream, thread-safe): both calls enqueue nothing and can
  * be used while a CUDA graph is captured. Close a region before its stream is destroyed (the
  * flag is keyed by the stream handle, which a later stream may reuse); at most 64 regions are
@@ -733,9 +735,10 @@ void zero_sched_destroy(zero_sched* s);
  *   scales; zeros up to a multiple of 32.
  * A record holds a whole row: any range of rows is a checkpoint of its own (row r0's address is
  * base + r0*ZERO_CKPT_ROW_BYTES(cols)), so checkpoints can be split among ranks by rows.
- * The calls of this section and the next are ordinary stream-ordered work: each waits for all
- * work before it on its stream. Between zero_overlap_begin and zero_overlap_end they count as
- * other work; close the region before a call of it reads what they write.
+ * The calls of this section and the next are stream-ordered: each waits for all work before it on
+ * its stream, the calls of an open overlap region included, and nothing behind it starts before
+ * it ends. Between zero_overlap_begin and zero_overlap_end they may read what the region's calls
+ * before them wrote; close the region before one of its calls reads what they write.
  * ---------------------------------------------------------------------------------------- */
 #define ZERO_CKPT_CODE_BYTES(cols) (((uint64_t)(cols) + 15u) / 16u * 16u)
 #define ZERO_CKPT_ROW_BYTES(cols) \

@@ -4,7 +4,8 @@
 // Order on the stream. Every kernel here waits for the kernel before it to complete before its
 // first access to memory (griddepcontrol.wait), and none lets the next kernel on the stream
 // start early, except a call's own second kernel: so a call is ordered like an ordinary launch,
-// also between the calls of a zero_overlap_begin/end region.
+// also between the calls of a zero_overlap_begin/end region. (There the kernel before it may be one
+// that ran alongside others; such a kernel completes only after all of them.)
 #pragma once
 
 #include <cuda_bf16.h>
