@@ -771,8 +771,9 @@ zero_status zero_ckpt_load_q8(uint64_t rows, uint64_t cols, const uint8_t* ckpt,
  * gives in that type (half a step of the type per term: for random data the error of dw against
  * the exact sum is 2.7e-4 of its size in fp16 and 2.1e-3 in bf16, where rounding dw alone makes
  * 2.1e-4 and 1.6e-3). Products are summed in binary32 on the tensor cores in an order fixed by
- * the sizes (the same call gives the same bits) and rounded once to dw's type. dw may point into a gradient bucket: it is what zero_step_fused and the bucket
- * schedulers take as a rank's gradient.
+ * the sizes (the same call gives the same bits) and rounded once to dw's type. An fp16 dw may
+ * point into a gradient bucket: it is what zero_step_fused and the bucket schedulers take as a
+ * rank's gradient. They read fp16 only: a bf16 dw is for a caller that converts it.
  *   dtype     : ZERO_F16 or ZERO_BF16, the type of dy and dw
  *   dy        : tokens x out_features, row stride lddy; dw: row stride lddw (elements). Aligned
  *               to their elements; 16-byte aligned rows of dy take the tensor-map loads.

@@ -325,3 +325,18 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
         for names, call in calls(dict(here, **{other: OnDevice(*shapes[other], device=0)})):
             with pytest.raises(TypeError if other in names.split() else lz.ZeroError):
                 call()
+
+
+def test_bf16_gradients_are_not_taken_for_fp16():
+    """The steps and buckets read fp16: a bf16 weight gradient is refused (n = 0 launches nothing)."""
+    torch = pytest.importorskip("torch")
+    g, f = torch.zeros(8, dtype=torch.bfloat16), torch.zeros(8)
+    p, st = torch.zeros(8, dtype=torch.float16), torch.zeros(1, dtype=torch.int32)
+    args = (f, f, f, f, f, f, p, lz.AdamHP(), 1, st)
+    lz.zero_step_fused(0, 1, [p], *args, stream=0)
+    lz.zero_step_fused(0, 1, [p.view(torch.int16)], *args, stream=0)
+    for bad in (lambda: lz.zero_step_fused(0, 1, [g], *args, stream=0),
+                lambda: lz.zero_step_fused(0, 2, [p, g], *args, stream=0),
+                lambda: lz.zero_quantize_q8(0, g, torch.zeros(0, dtype=torch.uint8), stream=0)):
+        with pytest.raises(TypeError):
+            bad()

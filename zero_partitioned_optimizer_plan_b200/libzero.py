@@ -249,11 +249,23 @@ _lib = _load()
 # ---------------------------------------------------------------------------------------------
 # marshalling helpers
 # ---------------------------------------------------------------------------------------------
+_bf16_types: dict = {}               # dtype -> is it bfloat16?
+
+
+def _is_bf16(dtype) -> bool:
+    known = _bf16_types.get(dtype)
+    if known is None:
+        known = _bf16_types[dtype] = str(dtype) == "torch.bfloat16"
+    return known
+
+
 def _ptr(x, elem_size: int | None = None) -> int:
     if x is None:
         return 0
     if hasattr(x, "data_ptr"):
-        if elem_size is not None and x.element_size() != elem_size:
+        # (2-byte operands are fp16, or its bits in an integer type)
+        if elem_size is not None and (x.element_size() != elem_size or
+                                      (elem_size == 2 and _is_bf16(x.dtype))):
             raise TypeError(f"expected a tensor of {elem_size}-byte elements, got {x.dtype}")
         if not x.is_contiguous():
             raise TypeError("tensor must be contiguous")
