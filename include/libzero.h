@@ -860,8 +860,12 @@ zero_status zero_block_join(const zero_block_desc* desc, const void* x, uint64_t
  *   t  = branch_scale * gate (.) gy;                 dh = gradient of post at h applied to t
  *   dpre_w = sum over rows of du (.) (y normalised), dpre_b = sum of du; dpost_w, dpost_b the
  *   same of t and h; dgate[k] = sum over gate row k's rows of branch_scale * gy (.) post(h)
- * The sums run in binary32 in an order fixed by the sizes (no atomics: the same call gives the
- * same bits) and are rounded once to dtype.
+ * The sums run in binary32 and are rounded once to dtype. Their order is fixed by the sizes, by
+ * whether dgate is asked for (it deals the rows out by gate rows) and by whether every matrix, the
+ * gate, the weights and the biases move in 16-byte accesses (one that does not changes the order
+ * for all). No atomics: the same call gives the same bits. At one alignment dx and dh have the
+ * same bits whatever else is asked for; the sums over rows (dgate, dpost_*, dpre_*) may be rounded
+ * otherwise with another set of outputs.
  *   y / y_ckpt : needed if du is given; h / h_ckpt: needed with a post_norm or dgate
  *   dx, dh, dgate (stride lddg), dpost_w, dpost_b, dpre_w, dpre_b: outputs, each may be NULL
  *                (not all of them); dgate needs a gate, dpost_* a branch (dh's rules), dpre_* a
