@@ -72,3 +72,86 @@ def _check(name, t, dw, want, mag, T):
                                    (5003, 1537, 1100), (2048, 64, 200)])
 def test_weight_gradient_at_unrounded_values(t, o, i, T):
     _check((t, o, i), t, *_call(t, o, i, T, t + o), T)
+
+
+# Pairs of CTAs that take several tiles one after the other, at both tile heights.
+def _plan(t, o, i):
+    """The library's plan: (256-row halves per tile, tiles along the out-features, along the
+    in-features, parts of the sum, units), with its measured constants, in binary32."""
+    f = torch.tensor
+    ti, kb, best = -(-i // 256), -(-t // 64), None
+    for m, stage, fixed in ((1, 0.47, 2.5), (2, 0.62, 4.0)):
+        to = -(-o // (256 * m))
+        for s in range(1, kb + 1):
+            if s > 1 and to * ti * s > 148:
+                break
+            blocks = -(-kb // s)
+            parts = -(-kb // blocks)
+            units = to * ti * parts
+            cost = f(float(-(-units // 74))) * (f(float(blocks)) * f(stage) + f(fixed))
+            if parts > 1:
+                cost = cost + f(3.0) + f(0.06) * f(float(units * m))
+            if best is None or float(cost) < best[0]:
+                best = (float(cost), m, to, ti, parts, units)
+    return best[1:]
+
+
+# (tokens, out, in, halves per tile, whether a pair takes a second unit, whether sums are split)
+SIZES = [
+    (70, 4500, 2500, 1, True, False),      # 180 tiles: both accumulators, ten tiles of in-features
+    (200, 4864, 2000, 2, True, False),     # 80 tiles of 512 rows
+    (700, 5000, 2304, 2, True, False),     # 90 of 11 stages: the ring of stages turns
+    (130, 4871, 2500, 2, True, False),     # dy through its aligned copy
+    (16384, 2304, 768, 2, False, True),    # a long sum in four parts
+    (16384, 2300, 760, 2, False, True),
+    (3000, 1003, 500, 1, False, True),
+]
+
+
+@pytest.mark.parametrize("t,o,i,halves,again,split", SIZES)
+def test_sizes_take_the_path_they_are_for(t, o, i, halves, again, split):
+    m, to, ti, parts, units = _plan(t, o, i)
+    assert (m, units > 74, parts > 1) == (halves, again, split)
+    need = to * ti * parts * 256 * m * 256 * 4 if parts > 1 else 0
+    if o % 8:
+        need += t * (-(-o // 8) * 8) * 2
+    assert lz.zero_ckpt_wgrad_q8_workspace(t, o, i) == need
+
+
+@pytest.mark.parametrize("T", [F16, BF16])
+@pytest.mark.parametrize("t,o,i", [c[:3] for c in SIZES])
+def test_several_tiles_per_pair(t, o, i, T):
+    _check((t, o, i), t, *_call(t, o, i, T, t + o), T)
+
+
+@pytest.mark.parametrize("t,o,i,pad,off,dwpad,dwoff", [
+    (200, 4864, 2000, 1, 0, 0, 0),         # 512-row tiles, dy loaded in place
+    (200, 4864, 2000, 0, 4, 0, 0),
+    (200, 4864, 2000, 8, 8, 3, 1),         # dw at any alignment
+    (130, 4871, 2501, 0, 0, 0, 0),
+    (130, 4871, 2501, 2, 3, 5, 3),
+    (70, 4500, 2500, 1, 1, 4, 2),          # 256-row tiles
+    (16384, 2304, 768, 3, 2, 1, 1)])
+@pytest.mark.parametrize("acc", [False, True])
+def test_strides(t, o, i, pad, off, dwpad, dwoff, acc):
+    dw, want, mag = _call(t, o, i, F16, 7, pad, off, dwpad, dwoff, acc)
+    _check((t, o, i, pad, acc), t, dw, want, mag, F16)
+    if dwpad or dwoff:
+        flat = dw._base.view(-1).clone()
+        flat.as_strided(dw.shape, dw.stride(), dw.storage_offset()).fill_(7.0)
+        assert bool((flat == 7).all())
+
+
+@pytest.mark.parametrize("t,o,i", [(16384, 2304, 768), (1024, 768, 768), (5003, 1537, 1100),
+                                   (700, 5000, 2304)])
+def test_same_bits_every_time(t, o, i):
+    dy = _rand(t, o, F16, 1, 0.05)
+    ck = torch.empty(t, lz.ckpt_row_bytes(i), dtype=torch.uint8, device=DEV)
+    lz.zero_ckpt_save_q8(t, i, _rand(t, i, F16, 2, 1.0), ck)
+    st = status_word()
+    n = lz.zero_ckpt_wgrad_q8_workspace(t, o, i)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV) if n else None
+    outs = [torch.empty(o, i, dtype=F16, device=DEV) for _ in range(12)]
+    for dw in outs:
+        lz.zero_ckpt_wgrad_q8(t, o, i, dy, ck, dw, st, workspace=ws)
+    assert all(torch.equal(dw, outs[0]) for dw in outs) and status_flags(st) == 0
