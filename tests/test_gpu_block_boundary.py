@@ -160,11 +160,81 @@ class Case:
         return out
 
 
+@pytest.mark.parametrize("pad,off", PADS)
+@pytest.mark.parametrize("T", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(9, 264), (160, 1032), (7, 768)])
+def test_forward_of_every_kind(rows, cols, T, pad, off):
+    for i, (post, pre) in enumerate(itertools.product(KINDS, KINDS)):
+        gate = [None, "row", "one", "copy"][(i + i // 4 + rows) % 4]
+        Case(rows, cols, T, post, pre, gate, i % 2 == 0, i, pad, off).forward(
+            i % 4 != 3, f"{post} {pre} {gate}")
+
+
+@pytest.mark.parametrize("pad,off", PADS)
+@pytest.mark.parametrize("T", [F16, BF16, F32])
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("gate", [None, "row", "one"])
+@pytest.mark.parametrize("rows,cols", [(11, 264), (10, 1000)])
+def test_backward_of_every_kind(rows, cols, T, pad, off, kept, gate):
+    for i, (post, pre) in enumerate(itertools.product(KINDS, KINDS)):
+        c = Case(rows, cols, T, post, pre, gate, i % 2 == 1, i, pad, off)
+        c.backward(kept, f"{post} {pre}")
+        if gate:                           # a gate whose gradient is not asked for
+            c.backward(kept, f"{post} {pre} without dgate", drop=("dgate",))
+
+
+# Rows enough for four turns and more of every team on 148 SMs: a turn is at most 3 CTAs of 8 warps
+# per SM in the forward pass, one of 16 in the gradient, and 256 or 512 columns per warp.
+MANY = [(768, 101, 71), (1000, 113, 61), (2048, 101, 41), (5000, 67, 31), (64, 211, 211)]
+
+
+@pytest.mark.parametrize("pad,off", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("T", [F16, BF16, F32])
+@pytest.mark.parametrize("cols,rows,times", MANY)
+def test_many_rows_forward(cols, rows, times, T, pad, off):
+    for i, (post, pre, gate) in enumerate([("none", "layer", None), ("rms", "rms", "copy"),
+                                           ("layer", "layer", "row"), ("rms", "layer", None)]):
+        Case(rows, cols, T, post, pre, gate, True, i, pad, off, times).forward(
+            i < 3, f"{post} {pre} {gate}")
+
+
+@pytest.mark.parametrize("pad,off", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("T", [F16, BF16, F32])
+@pytest.mark.parametrize("cols,rows,times", MANY)
+def test_many_rows_backward(cols, rows, times, T, pad, off):
+    for i, (post, pre, gate) in enumerate([("none", "layer", None), ("rms", "rms", "copy"),
+                                           ("layer", "layer", "row"), ("none", "rms", "one"),
+                                           ("rms", "layer", None)]):
+        Case(rows, cols, T, post, pre, gate, True, i, pad, off, times).backward(
+            T is not F32 and i % 2 == 0, f"{post} {pre} {gate}")
+
+
+@pytest.mark.parametrize("cols", [768, 2048, 1001, 8192])
+def test_many_rows_from_checkpoints(cols):
+    """The recomputation of a block's input, and a boundary of two checkpoints, over many rows."""
+    rows, times = 89, -(-70 * 768 // cols)
+    c = Case(rows, cols, F16, "rms", "layer", None, True, 3, 0, 0, times)
+    rec = [A.record(v.astype(np.float32)) for v in (c.x, c.h)]
+    cx, ch = (torch.from_numpy(r).to(DEV).repeat(times, 1) for r in rec)
+    xv, hv = (A.values(r, cols).astype(np.float64) for r in rec)
+    y, u = c.empty(), c.empty()
+    lz.zero_block_join(rows * times, cols, x_ckpt=cx, h_ckpt=ch, y=y, u=u, **c.kw)
+    wy, wu, my, mu = A.join(c.ref, xv, hv)
+    A.close("y", c.first("y", y), wy, my, F16, ROW_FWD)
+    A.close("u", c.first("u", u), wu, mu, F16, A.CHAIN)
+    alone = {k: v for k, v in c.ref.items() if not k.startswith("post")}
+    alone.update(post_norm="none", residual_scale=1.0)
+    kw = {k: v for k, v in c.kw.items() if k.startswith("pre")}
+    lz.zero_block_join(rows * times, cols, x_ckpt=cx, u=u, **kw)
+    _, wu, _, mu = A.join(alone, xv, None)
+    A.close("u alone", c.first("u", u), wu, mu, F16, A.CHAIN)
+
+
 @pytest.mark.parametrize("T", [F16, F32])
 @pytest.mark.parametrize("post,pre", [("layer", "rms"), ("none", "layer"), ("rms", "rms")])
 def test_outputs_asked_for(post, pre, T):
     """dx and dh have the same bits whatever else is asked for, and the same call the same bits; the
-    column sums of another set of outputs may be added in another order."""
+    column sums of another set of outputs may be rounded otherwise."""
     c = Case(53, 384, T, post, pre, "row", True, 5)
     full = c.backward(False)
     again = c.backward(False)
