@@ -1,6 +1,6 @@
 // Activation-side calls: geometry of the 8-bit checkpoint and the launchers' arguments, shared
-// by the argument checks (zero_act_api.cpp) and the kernels (zero_ckpt.cu, zero_join.cu,
-// zero_wgrad.cu). Internal.
+// by the argument checks (zero_act_api.cpp) and the kernels (zero_ckpt.cu, zero_join_*.cu,
+// zero_join_back_*.cu, zero_wgrad.cu). Internal.
 #pragma once
 
 #include <cstdint>

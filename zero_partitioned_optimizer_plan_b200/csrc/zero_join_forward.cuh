@@ -83,12 +83,17 @@ __device__ __forceinline__ void save_all(uint8_t* row, const CkptShape& s, uint3
     }
 }
 
-// A CTA has kW warps at most, 8 or (rows of more than 4096 columns) 16; still wider rows are
-// shared by the CTAs of a cluster.
+// A CTA has kW warps at most, 8 or 16 (rows of more than 4096 columns; of more than 2048 where
+// 32-bit values move singly, one chunk per lane); still wider rows are shared by the CTAs of a
+// cluster.
 
 // Rows on the way: many for one chunk per lane. Two 16-bit chunks per lane take one row ahead,
 // which with their registers held down (forward_ctas) lets three CTAs fit an SM: 8192 x 4096 bf16 with
 // both checkpoints 127 us, 16384 x 2048 fp16 101; with three rows ahead and two CTAs 149 and 107.
+// Where two CTAs fit either way, or one (wider rows, rows of any alignment, norms of two kinds, rows
+// from checkpoints, a norm alone), one row is as good or better: us with one and with three,
+//   4096 x 8192 fp16 51, 53      8192 x 1001 fp16 29, 31       16384 x 2048 mixed norms 76, 77
+//   16384 x 2048 from checkpoints 76, 80     norm alone 47, 50    4096 x 8192 with checkpoints 143, 142
 template <typename T, int kA, int G>
 struct ForwardShape {
     // post_w, post_b, pre_w, pre_b; two 32-bit chunks leave no room for them

@@ -13,18 +13,22 @@
 // A matrix product whose summation runs over the tokens, so both operands lie in memory with the
 // summation index as the slow one ("MN-major" tiles). Bound by the tensor cores for long sums.
 //
-// A pair of CTAs (two SMs, tcgen05 cta_group::2) computes 256 x 256 outputs, 64 tokens per stage:
-//   A  dy^T, 128 features per CTA, by TMA with the 128-byte swizzle (zeros outside the matrix);
-//      a dy with an out-feature count that is no multiple of 8 is first copied to aligned rows in
-//      the workspace (its rows' starts differ in alignment; loading it in place by the warps that
-//      make B took 117 us where the copy and the product take a third); one whose count is, but
-//      whose base or stride is not 16-byte aligned, is loaded in place.
+// A pair of CTAs (two SMs, tcgen05 cta_group::2) computes 256 x 256 or 512 x 256 outputs (kM = 1, 2
+// halves of 256 out-features), 64 tokens per stage:
+//   A  dy^T, 128 features per CTA and half, by TMA with the 128-byte swizzle (zeros outside the
+//      matrix); a dy with an out-feature count that is no multiple of 8 is first copied to aligned
+//      rows in the workspace (its rows' starts differ in alignment; loading it in place by the warps
+//      that make B took 117 us where the copy and the product take a third); one whose count is, but
+//      whose base or stride is not 16-byte aligned, is loaded in place, so that the workspace goes by
+//      the sizes alone and no usual call pays for a copy it does not need (16384 x 2304 x 768 with
+//      rows one value apart: one call 384 us, aligned 87).
 //   B  a, 128 features (one block of codes) per CTA. TMA brings the codes and their scales, eight
 //      warps form T(q*scale) as zero_ckpt_load_q8 does and store the tile swizzled. (Codes loaded
 //      by those warps into registers, stages ahead, were 4 times slower: the fence between their
 //      stores and the tensor cores also waits for every load in flight.)
-//   D  128 x 256 binary32 per CTA in tensor memory, two of them: four warps write one out while
-//      the next tile is computed.
+//   D  binary32 in tensor memory, written out by eight warps. kM = 1: 128 x 256 per CTA, two of
+//      them, one written out while the next tile is computed. kM = 2: 256 x 256 per CTA fill it;
+//      both halves use each converted tile of B, and the next tile waits for the write-out.
 // A cta_group::2 tile reads each half of B once for both SMs; the same tile of one CTA alone
 // (128 x 256) would need 3/2 of the shared-memory reads and twice the byte conversions.
 //
@@ -257,7 +261,7 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&v)[32]) {
 struct WgradCall {
     WgradArgs a;
     WgradPlan plan;
-    float* partial;      // splits > 1: [unit][256][256] binary32
+    float* partial;      // splits > 1: [unit][256 * m][256] binary32
     int vec;             // widest store into dw its base and stride allow, in bytes
 };
 
