@@ -155,3 +155,20 @@ def test_same_bits_every_time(t, o, i):
     for dw in outs:
         lz.zero_ckpt_wgrad_q8(t, o, i, dy, ck, dw, st, workspace=ws)
     assert all(torch.equal(dw, outs[0]) for dw in outs) and status_flags(st) == 0
+
+
+@pytest.mark.parametrize("o,stride", [(64, 1 << 41), (64, (1 << 41) + 3), (13, (1 << 40) + 1),
+                                      (64, 67)])
+def test_one_token_at_any_stride(o, stride):
+    """The stride of a single row is used for nothing, however large."""
+    i = 136
+    dy, a = _rand(1, o, F16, 1, 1.0), _rand(1, i, F16, 2, 1.0)
+    ck = torch.empty(1, lz.ckpt_row_bytes(i), dtype=torch.uint8, device=DEV)
+    lz.zero_ckpt_save_q8(1, i, a, ck)
+    n = lz.zero_ckpt_wgrad_q8_workspace(1, o, i)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV) if n else None
+    dw, st = torch.empty(o, i, dtype=F16, device=DEV), status_word()
+    lz.zero_ckpt_wgrad_q8(1, o, i, (dy.data_ptr(), stride), ck, dw, st, workspace=ws)
+    want = dy.double().T @ _values(ck, i)
+    _check((o, stride), 1, dw, want, want.abs(), F16)
+    assert status_flags(st) == 0

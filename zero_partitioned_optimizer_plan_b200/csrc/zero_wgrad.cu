@@ -805,7 +805,9 @@ cudaError_t run_wgrad(const WgradArgs& a, int dtype, void* ws, cudaStream_t stre
     c.partial = c.plan.splits > 1 ? (float*)ws : nullptr;
     c.vec = aligned16(a.dw.p) && a.dw.ld % 8 == 0 ? 16 : 2;
     if (a.tokens) {
-        bool tma = aligned16(a.dy.p) && a.dy.ld % 8 == 0;
+        // (a single row's stride is used for nothing: any, also one too large for a tensor map)
+        if (a.tokens == 1) c.a.dy.ld = ((uint64_t)a.outf + 7) / 8 * 8;
+        bool tma = aligned16(a.dy.p) && c.a.dy.ld % 8 == 0;
         if (!tma && a.outf % 8 != 0) {
             const uint32_t pitch = (a.outf + 7) / 8 * 8;
             uint16_t* copy = reinterpret_cast<uint16_t*>((char*)ws + partial_bytes(c.plan));
